@@ -196,6 +196,107 @@ fa_status_t fa_fwd_alibi(fa_handle_t h, const void* q, const void* k, const void
                          const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
                          void* o, float* lse, void* cuda_stream);
 
+/*
+ * A learned relative position bias by buckets (host struct, read during the
+ * call). The score of a visible pair is
+ *     scale * q.k + table[bucket_of[clip(rel, -reach, reach) + reach]][h],
+ * rel = j - (i + Skv_b - Sq_b): the key's signed distance from the row's
+ * diagonal anchored at the bottom-right corner, as in FA_ALIBI_RIGHT. The
+ * pages name no such bias; the map covers one- and two-sided, linear and
+ * logarithmic buckets alike.
+ * table      device fp32 [num_buckets, N] (an embedding's weight), finite.
+ * bucket_of  host int32[2 * reach + 1], each in [0, num_buckets).
+ * Limits: 1 <= reach <= 1024, 1 <= num_buckets <= 4096 (FA_ERR_UNSUPPORTED
+ * beyond). Distances past the reach take the buckets of its two ends.
+ */
+typedef struct {
+    const float* table;
+    const int32_t* bucket_of;
+    int32_t num_buckets;
+    int32_t reach;
+} fa_relbias_t;
+
+/*
+ * fa_fwd_relbias — fa_fwd with a learned relative position bias, for a handle
+ * without an attenMask kind (FA_ERR_UNSUPPORTED) and without an ALiBi variant
+ * (FA_ERR_PARAM_INVALID). The visibility rule is the sparseMode geometry,
+ * unchanged.
+ *
+ * The table is laid out by distance in the handle's workspace by a small
+ * kernel ahead of the attention kernel, in every call (it is a weight that
+ * changes between calls); the bucket map is uploaded when it differs from
+ * the last call's. The other arguments and the asynchronous behaviour are
+ * fa_fwd's. Errors: FA_ERR_NULLPTR (bias, table or bucket_of NULL),
+ * FA_ERR_PARAM_INVALID (a bucket outside the table, reach or num_buckets
+ * below 1, an unaligned table), FA_ERR_UNSUPPORTED on a stream that is being
+ * captured into a graph, and fa_fwd's.
+ */
+fa_status_t fa_fwd_relbias(fa_handle_t h, const void* q, const void* k, const void* v,
+                           const fa_relbias_t* bias, const int64_t* prefix,
+                           const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
+                           void* o, float* lse, void* cuda_stream);
+
+/*
+ * fa_bwd — the gradients of one forward: with P = exp(score - lse) over the
+ * visible pairs (0 elsewhere) and delta_i = sum_d d_o[i][d] o[i][d],
+ *     dV = P^T dO,                        dQ = scale * dS K,
+ *     dS = P * (dO V^T - delta + d_lse),  dK = scale * dS^T Q.
+ * The probabilities are recomputed tile by tile from q, k and lse; the score
+ * matrix is never written out. The pages describe only the forward; the
+ * formulas are the softmax's derivative.
+ *
+ * q, k, v, atten_mask, prefix, actual_seq_qlen, actual_seq_kvlen: as in the
+ *              fa_fwd call whose results o and lse are.
+ * d_o          device bf16, shape of o: the gradient of o.
+ * d_lse        device fp32, shape of lse: the gradient of lse, or NULL (0).
+ * dq, dk, dv   device bf16, shapes of q, k and v; every element is written.
+ *              Rows that see no key get dq = 0 and add nothing to dk and dv,
+ *              keys that no row sees get 0.
+ * All device operands 16-byte aligned, lse and d_lse 4-byte. Operands of a
+ * side without tokens (Sq or Skv 0) may be NULL.
+ * P and dS are rounded to bf16 for the products that sum over them, as the
+ * forward rounds P; all sums are fp32. Results are bitwise deterministic: dQ
+ * and dK, dV come from two passes, each output row from one CTA in a fixed
+ * order, at the price of recomputing the scores once more.
+ * The handle's work lists for the backward are kept beside the forward's, so
+ * alternating the two rebuilds neither. Device workspace, grown on the first
+ * calls: 1 KiB per 128 query rows and head, 64 bytes per 128 rows or keys and
+ * head, and the pre-pass's tables for a dense mask.
+ * Errors: fa_fwd's, and FA_ERR_PARAM_INVALID for a handle that names an ALiBi
+ * variant (fa_bwd_alibi), FA_ERR_UNSUPPORTED on a stream that is being
+ * captured into a graph (the work lists would be another call's at replay).
+ * Asynchronous like fa_fwd; fa_sync_status reports its device-side problems.
+ */
+fa_status_t fa_bwd(fa_handle_t h, const void* q, const void* k, const void* v,
+                   const uint8_t* atten_mask, const void* o, const float* lse, const void* d_o,
+                   const float* d_lse, const int64_t* prefix, const int64_t* actual_seq_qlen,
+                   const int64_t* actual_seq_kvlen, void* dq, void* dk, void* dv,
+                   void* cuda_stream);
+
+/* fa_bwd_alibi — fa_bwd for a handle whose descriptor names an ALiBi variant
+ * (the forward was fa_fwd_alibi with the same slopes, which are constants: no
+ * gradient of them is computed). Errors as fa_fwd_alibi and fa_bwd. */
+fa_status_t fa_bwd_alibi(fa_handle_t h, const void* q, const void* k, const void* v,
+                         const float* slopes, const void* o, const float* lse, const void* d_o,
+                         const float* d_lse, const int64_t* prefix,
+                         const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
+                         void* dq, void* dk, void* dv, void* cuda_stream);
+
+/*
+ * fa_bwd_relbias — fa_bwd after fa_fwd_relbias, with the bias's gradient
+ *     dtable[c][h] = sum of dS over the visible pairs in bucket c.
+ * dtable  device fp32 [num_buckets, N]; every element is written (0 for a
+ *         bucket no pair falls in). Summed in fp32 in a fixed order.
+ * The bias must be the forward's. Device workspace beside fa_bwd's:
+ * 4 * (2 * reach + 1) bytes per 128 query rows and head. Errors as
+ * fa_fwd_relbias and fa_bwd.
+ */
+fa_status_t fa_bwd_relbias(fa_handle_t h, const void* q, const void* k, const void* v,
+                           const fa_relbias_t* bias, const void* o, const float* lse,
+                           const void* d_o, const float* d_lse, const int64_t* prefix,
+                           const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
+                           void* dq, void* dk, void* dv, float* dtable, void* cuda_stream);
+
 /* fa_sync_status — wait for the handle's last call and read its device error
  * word: FA_OK, FA_ERR_TIMEOUT (a bounded wait in the kernel gave up, its
  * outputs are undefined) or FA_ERR_DEVICE. The error word is cleared. */

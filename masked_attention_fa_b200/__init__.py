@@ -10,6 +10,7 @@ The C entry points keep their names (``fa_create``, ``fa_fwd``, ...). The
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -65,6 +66,15 @@ class fa_split_part_t(ctypes.Structure):
     ]
 
 
+class fa_relbias_t(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("bucket_of", ctypes.POINTER(ctypes.c_int32)),
+        ("num_buckets", ctypes.c_int32),
+        ("reach", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -87,6 +97,15 @@ def load_library():
     lib.fa_fwd.restype = st
     lib.fa_fwd_alibi.argtypes = [P, P, P, P, P, i64p, i64p, i64p, P, P, P]
     lib.fa_fwd_alibi.restype = st
+    rp = ctypes.POINTER(fa_relbias_t)
+    lib.fa_fwd_relbias.argtypes = [P, P, P, P, rp, i64p, i64p, i64p, P, P, P]
+    lib.fa_fwd_relbias.restype = st
+    lib.fa_bwd.argtypes = [P, P, P, P, P, P, P, P, P, i64p, i64p, i64p, P, P, P, P]
+    lib.fa_bwd.restype = st
+    lib.fa_bwd_alibi.argtypes = [P, P, P, P, P, P, P, P, P, i64p, i64p, i64p, P, P, P, P]
+    lib.fa_bwd_alibi.restype = st
+    lib.fa_bwd_relbias.argtypes = [P, P, P, P, rp, P, P, P, P, i64p, i64p, i64p, P, P, P, P, P]
+    lib.fa_bwd_relbias.restype = st
     lib.fa_sync_status.argtypes = [P]
     lib.fa_sync_status.restype = st
     lib.fa_destroy.argtypes = [P]
@@ -128,7 +147,8 @@ def load_library():
 EXPORTED = ("fa_create", "fa_fwd", "fa_sync_status", "fa_destroy", "fa_last_error",
             "fa_version", "fa_validate", "fa_visible_pairs", "fa_tile_class", "fa_plan_stats",
             "fa_plan_items", "fa_fwd_noalloc", "fa_split_queries", "fa_mask_occupancy",
-            "fa_fwd_with_ranges", "fa_fwd_paged", "fa_noalloc_sync_status", "fa_fwd_alibi")
+            "fa_fwd_with_ranges", "fa_fwd_paged", "fa_noalloc_sync_status", "fa_fwd_alibi",
+            "fa_fwd_relbias", "fa_bwd", "fa_bwd_alibi", "fa_bwd_relbias")
 
 
 def _check(status):
@@ -272,6 +292,80 @@ def fa_fwd_alibi(h, q, k, v, slopes, o, lse, prefix=None, actual_seq_qlen=None,
                                        ctypes.c_void_p(_stream_int(stream, q.device))))
 
 
+def _relbias(table, bucket_of):
+    """(fa_relbias_t, the int32 array it points into) of a table [num_buckets,
+    N] and a bucket map of 2 * reach + 1 entries."""
+    m = np.ascontiguousarray(bucket_of, dtype=np.int32)
+    if m.ndim != 1 or m.size < 3 or m.size % 2 == 0:
+        raise ValueError("the bucket map must have 2 * reach + 1 entries, reach >= 1")
+    b = fa_relbias_t(table.data_ptr(), m.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)),
+                     int(table.shape[0]), m.size // 2)
+    return b, m
+
+
+def relative_buckets(num_buckets, max_distance, bidirectional=True):
+    """Bucket map int32 [2 * max_distance + 1] of the usual logarithmic
+    buckets: entry rel + max_distance is the bucket of the distance rel = key
+    - query. Two-sided maps give each side half of the buckets (rel > 0 the
+    upper half); one-sided maps put every rel > 0 into bucket 0. Half of a
+    side's buckets hold one distance each, the others grow with the logarithm
+    of the distance up to max_distance (a boundary within 1e-9 of a whole
+    number counts as that number)."""
+    side = num_buckets // 2 if bidirectional else num_buckets
+    single = side // 2
+    if single < 1 or max_distance <= single:
+        raise ValueError("need two buckets a side and max_distance above its single distances")
+    rel = np.arange(-max_distance, max_distance + 1)
+    d = np.abs(rel) if bidirectional else np.maximum(-rel, 0)
+    grow = np.log(np.maximum(d, single) / single) / np.log(max_distance / single)
+    far = single + np.floor(grow * (side - single) + 1e-9).astype(np.int64)
+    bucket = np.where(d < single, d, np.minimum(far, side - 1))
+    if bidirectional:
+        bucket = bucket + side * (rel > 0)
+    return bucket.astype(np.int32)
+
+
+def fa_fwd_relbias(h, q, k, v, table, bucket_of, o, lse, prefix=None, actual_seq_qlen=None,
+                   actual_seq_kvlen=None, stream=None):
+    """fa_fwd with a learned relative position bias; table: fp32 CUDA tensor
+    [num_buckets, N], bucket_of: host int32 [2 * reach + 1]."""
+    a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
+    b, keep = _relbias(table, bucket_of)
+    _check(load_library().fa_fwd_relbias(h, _ptr(q), _ptr(k), _ptr(v), ctypes.byref(b), *a.ptrs(),
+                                         _ptr(o), _ptr(lse),
+                                         ctypes.c_void_p(_stream_int(stream, q.device))))
+
+
+def fa_bwd(h, q, k, v, o, lse, d_o, dq, dk, dv, atten_mask=None, d_lse=None, prefix=None,
+           actual_seq_qlen=None, actual_seq_kvlen=None, stream=None):
+    """Enqueue one backward (see include/fa.h). Tensors must be CUDA tensors."""
+    a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
+    _check(load_library().fa_bwd(h, _ptr(q), _ptr(k), _ptr(v), _ptr(atten_mask), _ptr(o),
+                                 _ptr(lse), _ptr(d_o), _ptr(d_lse), *a.ptrs(), _ptr(dq), _ptr(dk),
+                                 _ptr(dv), ctypes.c_void_p(_stream_int(stream, q.device))))
+
+
+def fa_bwd_alibi(h, q, k, v, slopes, o, lse, d_o, dq, dk, dv, d_lse=None, prefix=None,
+                 actual_seq_qlen=None, actual_seq_kvlen=None, stream=None):
+    """fa_bwd for a handle with an ALiBi variant; slopes: fp32 CUDA tensor [N]."""
+    a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
+    _check(load_library().fa_bwd_alibi(h, _ptr(q), _ptr(k), _ptr(v), _ptr(slopes), _ptr(o),
+                                       _ptr(lse), _ptr(d_o), _ptr(d_lse), *a.ptrs(), _ptr(dq),
+                                       _ptr(dk), _ptr(dv),
+                                       ctypes.c_void_p(_stream_int(stream, q.device))))
+
+
+def fa_bwd_relbias(h, q, k, v, table, bucket_of, o, lse, d_o, dq, dk, dv, dtable, d_lse=None,
+                   prefix=None, actual_seq_qlen=None, actual_seq_kvlen=None, stream=None):
+    """fa_bwd after fa_fwd_relbias; dtable: fp32 CUDA tensor [num_buckets, N]."""
+    a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
+    b, keep = _relbias(table, bucket_of)
+    _check(load_library().fa_bwd_relbias(h, _ptr(q), _ptr(k), _ptr(v), ctypes.byref(b), _ptr(o),
+                                         _ptr(lse), _ptr(d_o), _ptr(d_lse), *a.ptrs(), _ptr(dq),
+                                         _ptr(dk), _ptr(dv), _ptr(dtable),
+                                         ctypes.c_void_p(_stream_int(stream, q.device))))
+
+
 def _stream_int(stream, device):
     import torch
     if stream is None:
@@ -402,8 +496,12 @@ class MaskedAttention:
 
     def __call__(self, q, k, v, atten_mask=None, prefix=None, actual_seq_qlen=None,
                  actual_seq_kvlen=None, out=None, lse=None, stream=None, ranges=None,
-                 slopes=None):
+                 slopes=None, rel_bias=None, rel_buckets=None):
         import torch
+        if rel_bias is not None:
+            return self._relbias_forward(q, k, v, rel_bias, rel_buckets, atten_mask, ranges,
+                                         slopes, prefix, actual_seq_qlen, actual_seq_kvlen, out,
+                                         lse, stream)
         oshape, lshape = self.out_shapes()
         if out is None:
             out = torch.empty(oshape, dtype=torch.bfloat16, device=q.device)
@@ -428,6 +526,119 @@ class MaskedAttention:
             fa_fwd(self.handle, q, k, v, out, lse, atten_mask, prefix, actual_seq_qlen,
                    actual_seq_kvlen, stream)
         return out, lse
+
+    def kv_shape(self):
+        d = self.desc
+        if self.layout == "BNSD":
+            return (d.B, d.N, d.Skv, d.D)
+        if self.layout == "BSND":
+            return (d.B, d.Skv, d.N, d.D)
+        return (d.Skv, d.N, d.D)
+
+    def _mask_shape(self):
+        d = self.desc
+        return {FA_MASK_SS: (d.Sq, d.Skv), FA_MASK_B1SS: (d.B, 1, d.Sq, d.Skv),
+                FA_MASK_BNSS: (d.B, d.N, d.Sq, d.Skv)}.get(d.mask_kind)
+
+    @staticmethod
+    def _need(device, **tensors):
+        """Each given as name=(tensor, dtypes, shape): contiguous, on `device`."""
+        import torch
+        for name, (t, dtypes, shape) in tensors.items():
+            if t is None:
+                continue
+            dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+            if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_contiguous()
+                    or not t.is_cuda or t.device != device or tuple(t.shape) != tuple(shape)):
+                raise ValueError(f"{name} must be a contiguous {dtypes[0]} CUDA tensor of shape "
+                                 f"{tuple(shape)} on {device}")
+
+    def _need_bias(self, device, rel_bias, rel_buckets):
+        import torch
+        if rel_buckets is None:
+            raise ValueError("rel_bias needs rel_buckets, its bucket map")
+        if not isinstance(rel_bias, torch.Tensor) or rel_bias.dim() != 2:
+            raise ValueError("rel_bias must be a tensor [num_buckets, N]")
+        self._need(device, rel_bias=(rel_bias, torch.float32, (rel_bias.shape[0], self.desc.N)))
+
+    @staticmethod
+    @contextlib.contextmanager
+    def _on(stream, device, *inputs):
+        """The tensors' device current, and `stream` (None: torch's current
+        one) current too, so that what is allocated belongs to it; tensors of
+        other streams are kept from reuse until this stream has read them."""
+        import torch
+        with torch.cuda.device(device):
+            here = torch.cuda.current_stream(device)
+            if stream is None:
+                stream = here
+            elif not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            with torch.cuda.stream(stream):
+                yield stream
+            if stream != here:
+                for t in inputs:
+                    if t is not None:
+                        t.record_stream(stream)
+
+    def _relbias_forward(self, q, k, v, rel_bias, rel_buckets, atten_mask, ranges, slopes, prefix,
+                         actual_seq_qlen, actual_seq_kvlen, out, lse, stream):
+        import torch
+        if atten_mask is not None or ranges is not None or slopes is not None:
+            raise ValueError("rel_bias goes with neither atten_mask, ranges nor slopes")
+        oshape, lshape = self.out_shapes()
+        bf16, dev = torch.bfloat16, q.device
+        self._need(dev, q=(q, bf16, oshape), k=(k, bf16, self.kv_shape()),
+                   v=(v, bf16, self.kv_shape()), out=(out, bf16, oshape),
+                   lse=(lse, torch.float32, lshape))
+        self._need_bias(dev, rel_bias, rel_buckets)
+        with self._on(stream, dev, q, k, v, rel_bias, out, lse) as s:
+            out = torch.empty(oshape, dtype=bf16, device=dev) if out is None else out
+            lse = torch.empty(lshape, dtype=torch.float32, device=dev) if lse is None else lse
+            fa_fwd_relbias(self.handle, q, k, v, rel_bias, rel_buckets, out, lse, prefix,
+                           actual_seq_qlen, actual_seq_kvlen, s)
+        return out, lse
+
+    def backward(self, d_o, q, k, v, o, lse, atten_mask=None, prefix=None, actual_seq_qlen=None,
+                 actual_seq_kvlen=None, d_lse=None, slopes=None, rel_bias=None, rel_buckets=None,
+                 dq=None, dk=None, dv=None, d_rel_bias=None, stream=None):
+        """Gradients of ``o, lse = attn(q, k, v, ...)`` called with the same
+        arguments: (dq, dk, dv), and d_rel_bias with a learned bias (see
+        fa_bwd in include/fa.h). d_o, d_lse: the gradients of o and lse (d_lse
+        None: 0)."""
+        import torch
+        oshape, lshape = self.out_shapes()
+        kshape = self.kv_shape()
+        bf16, f32, dev = torch.bfloat16, torch.float32, q.device
+        self._need(dev, q=(q, bf16, oshape), k=(k, bf16, kshape), v=(v, bf16, kshape),
+                   o=(o, bf16, oshape), d_o=(d_o, bf16, oshape), lse=(lse, f32, lshape),
+                   d_lse=(d_lse, f32, lshape), dq=(dq, bf16, oshape), dk=(dk, bf16, kshape),
+                   dv=(dv, bf16, kshape), slopes=(slopes, f32, (self.desc.N,)))
+        if atten_mask is not None and self._mask_shape() is not None:
+            self._need(dev, atten_mask=(atten_mask, (torch.uint8, torch.bool), self._mask_shape()))
+        if rel_bias is not None:
+            if atten_mask is not None or slopes is not None:
+                raise ValueError("rel_bias goes with neither atten_mask nor slopes")
+            self._need_bias(dev, rel_bias, rel_buckets)
+            self._need(dev, d_rel_bias=(d_rel_bias, f32, rel_bias.shape))
+        with self._on(stream, dev, d_o, q, k, v, o, lse, atten_mask, d_lse, slopes, rel_bias, dq, dk,
+                      dv, d_rel_bias) as s:
+            dq = torch.empty(oshape, dtype=bf16, device=dev) if dq is None else dq
+            dk = torch.empty(kshape, dtype=bf16, device=dev) if dk is None else dk
+            dv = torch.empty(kshape, dtype=bf16, device=dev) if dv is None else dv
+            lens = dict(d_lse=d_lse, prefix=prefix, actual_seq_qlen=actual_seq_qlen,
+                        actual_seq_kvlen=actual_seq_kvlen, stream=s)
+            if rel_bias is not None:
+                if d_rel_bias is None:
+                    d_rel_bias = torch.empty(rel_bias.shape, dtype=f32, device=dev)
+                fa_bwd_relbias(self.handle, q, k, v, rel_bias, rel_buckets, o, lse, d_o, dq, dk,
+                               dv, d_rel_bias, **lens)
+                return dq, dk, dv, d_rel_bias
+            if slopes is not None:
+                fa_bwd_alibi(self.handle, q, k, v, slopes, o, lse, d_o, dq, dk, dv, **lens)
+            else:
+                fa_bwd(self.handle, q, k, v, o, lse, d_o, dq, dk, dv, atten_mask=atten_mask, **lens)
+        return dq, dk, dv
 
     def paged(self, q, k_cache, v_cache, block_table, actual_seq_qlen, actual_seq_kvlen,
               prefix=None, out=None, lse=None, stream=None):

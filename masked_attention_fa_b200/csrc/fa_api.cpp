@@ -11,53 +11,24 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <new>
 #include <vector>
 
 #include "../../include/fa.h"
+#include "fa_handle.h"
 #include "fa_kernel.h"
 #include "fa_plan.h"
 
 using namespace fa;
 
-struct fa_handle_s {
-  fa_desc_t desc{};
-  int device = -1;
-  int num_sms = 0;
-  // plan cache: the per-call arrays the current work list was built from
-  std::vector<int64_t> plan_key;
-  bool plan_valid = false;
-  int32_t n_items = 0;
-  int32_t n_seqs = 0;
-  SeqRec geo0{};  // geometry of sequence 0 (every sequence's, outside TND)
-  // paged K/V calls: [header][SeqRec x B][PagedGroup x n_groups][PagedUnit x
-  // n_units] then the units' partial results (the plan key starts with -2)
-  int32_t n_groups = 0;
-  int64_t n_units = 0;
-  int32_t paged_rows = 0;  // most query rows in one group
-  // device workspace: [error word | claim counter at 128 | claim_done at 192 |
-  // pad to 256 B][SeqRec x B][WorkItem x n]
-  // [item_tr: 2 x TileRange per item] then, for a dense attenMask, the
-  // occupancy pre-pass's ranges and classes
-  void* d_ws = nullptr;
-  size_t ws_bytes = 0;
-  // pinned staging of the work list and the event of its last upload
-  void* h_stage = nullptr;
-  size_t stage_bytes = 0;
-  cudaEvent_t stage_done = nullptr;
-  cudaEvent_t last_call = nullptr;
-  bool any_call = false;
-  // tensor maps of the last call's operands
-  const void* tm_key[3] = {nullptr, nullptr, nullptr};
-  CUtensorMap tm[3];
-  uint64_t timeout_ns = 2000000000ull;
-  uint32_t debug_flags = 0;
-};
-
 namespace {
 
-constexpr size_t kHeaderBytes = 256;
 constexpr size_t kClaimOffset = 128;  // two work-claim counters, 64 bytes apart
+
+}  // namespace
+
+namespace fa {
 
 bool env_flag(const char* name) {
   const char* v = std::getenv(name);
@@ -68,8 +39,6 @@ fa_status_t cuda_fail(cudaError_t e, const char* what) {
   return fail(FA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 // Planes of the attenMask the occupancy pre-pass reduces: SS one plane for
 // every batch and head, B1SS one per batch, BNSS one per batch and head; 0
 // when the call reads no mask.
@@ -79,6 +48,10 @@ int64_t mask_planes(const fa_desc_t* d, int has_mask) {
   if (d->mask_kind == FA_MASK_B1SS) return d->B;
   return d->B * d->N;
 }
+
+}  // namespace fa
+
+namespace {
 
 // Dense-mask calls keep, after the work list, each item's two ranges
 // (item_tr, 32 bytes per item) and then the pre-pass's scratch.
@@ -98,6 +71,10 @@ void occupancy_bind(OccParams* a, uint8_t* scratch) {
   a->ranges = reinterpret_cast<TileRange*>(scratch);
   a->cls = scratch + align_up((size_t)(a->n_planes * a->n_qt) * sizeof(TileRange), 256);
 }
+
+}  // namespace
+
+namespace fa {
 
 fa_status_t bind_device(fa_handle_t h) {
   int dev = 0;
@@ -124,6 +101,7 @@ fa_status_t bind_device(fa_handle_t h) {
   return FA_OK;
 }
 
+
 // Make sure the device workspace holds `bytes`; the error word is zeroed
 // whenever the workspace is (re)allocated.
 fa_status_t ensure_workspace(fa_handle_t h, size_t bytes) {
@@ -147,6 +125,10 @@ fa_status_t ensure_workspace(fa_handle_t h, size_t bytes) {
   return FA_OK;
 }
 
+}  // namespace fa
+
+namespace {
+
 fa_status_t ensure_stage(fa_handle_t h, size_t bytes) {
   if (h->h_stage != nullptr && h->stage_bytes >= bytes) return FA_OK;
   if (h->h_stage != nullptr) {
@@ -165,6 +147,10 @@ fa_status_t ensure_stage(fa_handle_t h, size_t bytes) {
   return FA_OK;
 }
 
+}  // namespace
+
+namespace fa {
+
 std::vector<int64_t> make_key(const fa_desc_t* d, const int64_t* prefix, const int64_t* cu_q,
                               const int64_t* cu_kv, int has_mask) {
   std::vector<int64_t> key;
@@ -176,6 +162,10 @@ std::vector<int64_t> make_key(const fa_desc_t* d, const int64_t* prefix, const i
   }
   return key;
 }
+
+}  // namespace fa
+
+namespace {
 
 fa_status_t refresh_plan(fa_handle_t h, const int64_t* prefix, const int64_t* cu_q,
                          const int64_t* cu_kv, int has_mask, cudaStream_t stream) {
@@ -238,6 +228,10 @@ fa_status_t refresh_plan(fa_handle_t h, const int64_t* prefix, const int64_t* cu
   return FA_OK;
 }
 
+}  // namespace
+
+namespace fa {
+
 // Element strides (batch, head, token) of Q/O or K/V in the handle's layout.
 void operand_strides(const fa_desc_t* d, int64_t S, int64_t* sb, int64_t* sh, int64_t* st) {
   const int64_t N = d->N, D = d->D;
@@ -259,6 +253,10 @@ void operand_strides(const fa_desc_t* d, int64_t S, int64_t* sb, int64_t* sh, in
       break;
   }
 }
+
+}  // namespace fa
+
+namespace {
 
 fa_status_t encode_maps(fa_handle_t h, const void* q, const void* k, const void* v) {
   const void* ptrs[3] = {q, k, v};
@@ -312,7 +310,7 @@ namespace {
 // occupancy of this mask, already computed by fa_mask_occupancy.
 fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
                     const uint8_t* atten_mask, const int32_t* ranges, const float* slopes,
-                    const int64_t* prefix, const int64_t* actual_seq_qlen,
+                    const fa_relbias_t* bias, const int64_t* prefix, const int64_t* actual_seq_qlen,
                     const int64_t* actual_seq_kvlen, void* o, float* lse, void* cuda_stream) {
   if (!h) return fail(FA_ERR_NULLPTR, "handle is NULL");
   if (!q || !k || !v || !o || !lse) return fail(FA_ERR_NULLPTR, "q, k, v, o and lse are required");
@@ -332,6 +330,10 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
   st = bind_device(h);
   if (st != FA_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  if (bias) {
+    st = refuse_capture(stream);
+    if (st != FA_OK) return st;
+  }
   st = refresh_plan(h, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask, stream);
   if (st != FA_OK) return st;
   if (h->n_items == 0) return FA_OK;  // no query rows: nothing to write
@@ -419,6 +421,10 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
     p.slopes = slopes;
     p.alibi = d->alibi;
   }
+  if (bias) {
+    st = prepare_rel(h, bias, stream, &p.rel);
+    if (st != FA_OK) return st;
+  }
   p.tnd = d->layout == FA_TND ? 1 : 0;
   p.scale_log2 = (float)(d->scale * 1.4426950408889634073599);
   p.debug_flags = h->debug_flags;
@@ -445,7 +451,7 @@ fa_status_t fa_fwd(fa_handle_t h, const void* q, const void* k, const void* v,
                    const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen, void* o,
                    float* lse, void* cuda_stream) {
   clear_error();
-  return forward(h, q, k, v, atten_mask, nullptr, nullptr, prefix, actual_seq_qlen,
+  return forward(h, q, k, v, atten_mask, nullptr, nullptr, nullptr, prefix, actual_seq_qlen,
                  actual_seq_kvlen, o, lse, cuda_stream);
 }
 
@@ -458,8 +464,24 @@ fa_status_t fa_fwd_alibi(fa_handle_t h, const void* q, const void* k, const void
   if (!slopes) return fail(FA_ERR_NULLPTR, "slopes is NULL");
   if (h->desc.alibi == FA_ALIBI_NONE)
     return fail(FA_ERR_PARAM_INVALID, "fa_fwd_alibi needs a handle with an ALiBi variant");
-  return forward(h, q, k, v, nullptr, nullptr, slopes, prefix, actual_seq_qlen,
+  return forward(h, q, k, v, nullptr, nullptr, slopes, nullptr, prefix, actual_seq_qlen,
                  actual_seq_kvlen, o, lse, cuda_stream);
+}
+
+fa_status_t fa_fwd_relbias(fa_handle_t h, const void* q, const void* k, const void* v,
+                           const fa_relbias_t* bias, const int64_t* prefix,
+                           const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
+                           void* o, float* lse, void* cuda_stream) {
+  clear_error();
+  if (!h) return fail(FA_ERR_NULLPTR, "handle is NULL");
+  fa_status_t st = validate_rel(&h->desc, bias);
+  if (st != FA_OK) return st;
+  try {
+    return forward(h, q, k, v, nullptr, nullptr, nullptr, bias, prefix, actual_seq_qlen,
+                   actual_seq_kvlen, o, lse, cuda_stream);
+  } catch (const std::exception& e) {
+    return fail(FA_ERR_ALLOC, "host allocation: %s", e.what());
+  }
 }
 
 fa_status_t fa_fwd_with_ranges(fa_handle_t h, const void* q, const void* k, const void* v,
@@ -472,7 +494,7 @@ fa_status_t fa_fwd_with_ranges(fa_handle_t h, const void* q, const void* k, cons
                 "fa_fwd_with_ranges needs sparse_mode 0 or 1 with a mask kind and atten_mask");
   if (!ranges) return fail(FA_ERR_NULLPTR, "ranges is NULL");
   if ((uintptr_t)ranges & 15u) return fail(FA_ERR_PARAM_INVALID, "ranges must be 16-byte aligned");
-  return forward(h, q, k, v, atten_mask, ranges, nullptr, nullptr, nullptr, nullptr, o, lse,
+  return forward(h, q, k, v, atten_mask, ranges, nullptr, nullptr, nullptr, nullptr, nullptr, o, lse,
                  cuda_stream);
 }
 
@@ -655,6 +677,7 @@ fa_status_t fa_destroy(fa_handle_t h) {
   if (h->h_stage) cudaFreeHost(h->h_stage);
   if (h->stage_done) cudaEventDestroy(h->stage_done);
   if (h->last_call) cudaEventDestroy(h->last_call);
+  release_training(h);
   delete h;
   return FA_OK;
 }

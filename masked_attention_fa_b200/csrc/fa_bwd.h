@@ -1,0 +1,126 @@
+// Structures and launch interface of the backward pass and of the learned
+// relative position bias.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <vector>
+
+#include "fa_internal.h"
+#include "fa_kernel.h"
+
+namespace fa {
+
+// Work item of a backward kernel: one (sequence, head, 128-row tile). In the
+// query list the tile is 128 query rows and [lo, hi) are its key tiles; in
+// the key list it is 128 keys and [lo, hi) are its query tiles. Tiles in
+// [full_lo, full_hi) need no element mask.
+struct BwdItem {
+  int32_t b, h, tile;
+  int32_t stat;  // row-statistics block: the tile's own (query list), or that
+                 // of the (sequence, head)'s query tile 0 (key list)
+  int32_t lo, hi, full_lo, full_hi;
+};
+static_assert(sizeof(BwdItem) == 32, "BwdItem layout");
+
+// Query tiles that see keys [c0, c0 + 128) of sequence s: [lo, hi) holds
+// every tile with a visible pair; in [full_lo, full_hi) every stored row sees
+// every stored key of the tile (keys past the sequence's end are not stored
+// and rows past its end have zero weight, so neither needs a mask).
+FA_HD TileRange key_tile_rows(const SeqRec& s, int64_t c0) {
+  TileRange t{0, 0, 0, 0};
+  if (c0 >= s.skv || s.sq <= 0) return t;
+  const int64_t c1 = imin64(c0 + kTileN, s.skv) - 1;  // last stored key
+  // Row i sees key j when i >= j - hi_off (any i for j < prefix) and
+  // i <= j - lo_off.
+  const int64_t i_first = s.prefix > c0 ? 0 : imax64(0, c0 - s.hi_off);
+  const int64_t i_last = imin64(int64_t(s.sq) - 1, c1 - s.lo_off);
+  if (i_first > i_last) return t;
+  t.lo = int32_t(i_first / kTileM);
+  t.hi = int32_t(i_last / kTileM + 1);
+  t.full_lo = t.full_hi = t.lo;
+  if (s.flags & kSeqDenseMask) return t;
+  const int64_t a = s.prefix > c1 ? 0 : imax64(0, c1 - s.hi_off);
+  const int64_t z = imin64(int64_t(s.sq) - 1, c0 - s.lo_off);  // last row that sees key c0
+  if (a > z) return t;
+  int64_t f_lo = (a + kTileM - 1) / kTileM;
+  int64_t f_hi = z == int64_t(s.sq) - 1 ? z / kTileM + 1 : (z + 1) / kTileM;
+  f_lo = imax64(f_lo, t.lo);
+  f_hi = imin64(f_hi, t.hi);
+  if (f_hi > f_lo) {
+    t.full_lo = int32_t(f_lo);
+    t.full_hi = int32_t(f_hi);
+  }
+  return t;
+}
+
+// Expand table [num_buckets][N] into ext.
+cudaError_t launch_rel_expand(const float* table, const int32_t* bucket_of, float* ext, int32_t N,
+                              int32_t num_buckets, int32_t reach, cudaStream_t stream);
+
+// ------------------------------------------------------------- the backward
+struct __align__(64) BwdParams {
+  CUtensorMap tm_q, tm_k, tm_v, tm_do;
+  const SeqRec* seqs;
+  const BwdItem* q_items;
+  const BwdItem* k_items;
+  // Row statistics, one block of 2 x 128 floats per query tile: the negated
+  // lse in log2 units (-inf for rows that see no key or are not stored, so
+  // that their weights are 0 without a mask), then dlse - delta.
+  float* stats;
+  const uint8_t* mask;       // dense attenMask, else null
+  unsigned int* err_word;
+  const void* q;             // bf16 operands and gradients, one layout
+  const void* k;
+  const void* v;
+  const void* o;
+  const void* d_o;
+  const float* lse;
+  const float* d_lse;        // or null
+  void* dq;
+  void* dk;
+  void* dv;
+  const float* slopes;       // ALiBi, else null
+  RelBias rel;
+  // Gradient of the bias by distance: one row of 2 reach + 1 sums per query
+  // tile (indexed by its statistics block), else null.
+  float* rel_part;
+  int64_t q_sb, q_sh, q_st;  // element strides of Q, O and their gradients
+  int64_t k_sb, k_sh, k_st;  // of K, V and their gradients
+  int64_t l_sb, l_sh;        // of lse
+  int64_t m_sb, m_sh, m_si;  // of the mask
+  int32_t alibi;             // fa_alibi_t
+  int32_t n_q, n_k;          // items
+  int32_t tnd;
+  float scale, scale_log2;
+  uint64_t timeout_ns;
+};
+
+// Row statistics of every query tile (see BwdParams::stats).
+cudaError_t launch_bwd_stats(int D, const BwdParams& p, cudaStream_t stream);
+// dQ (and rel_part), then dK and dV.
+cudaError_t launch_bwd(int D, const BwdParams& p, int num_sms, cudaStream_t stream,
+                       const char** why);
+
+// Dense masks: copies the occupancy pre-pass's key-tile ranges into the
+// query items and reduces its classes to the key items' query-tile ranges.
+struct BwdOccParams {
+  const TileRange* ranges;  // [plane][n_qt]
+  const uint8_t* cls;       // [plane][n_qt][n_kt]
+  BwdItem* q_items;
+  BwdItem* k_items;
+  int64_t occ_sb, occ_sh;   // plane = b * occ_sb + h * occ_sh
+  int32_t n_q, n_k, n_qt, n_kt;
+};
+cudaError_t launch_bwd_ranges(const BwdOccParams& a, cudaStream_t stream);
+
+// dtable[c][h] = the sum of rel_part over head h's query tiles (rows
+// [h * tiles, (h + 1) * tiles) of rel_part) and the distances of bucket c, in
+// a fixed order. dist: scratch, fp32 [N][2 reach + 1].
+cudaError_t launch_rel_reduce(const float* rel_part, float* dist, const int32_t* bucket_of,
+                              float* dtable, int32_t N, int32_t tiles, int32_t num_buckets,
+                              int32_t reach, cudaStream_t stream);
+
+}  // namespace fa

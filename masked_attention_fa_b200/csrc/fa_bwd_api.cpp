@@ -1,0 +1,409 @@
+// C ABI front end of the backward pass and of the relative position bias's
+// device tables: checks, work lists, scratch and launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+#include <exception>
+#include <vector>
+
+#include "../../include/fa.h"
+#include "fa_bwd.h"
+#include "fa_handle.h"
+#include "fa_kernel.h"
+#include "fa_plan.h"
+
+using namespace fa;
+
+namespace fa {
+
+fa_status_t ensure_buffer(fa_handle_t h, DeviceBuffer* buf, size_t bytes) {
+  if (buf->ptr != nullptr && buf->bytes >= bytes) return FA_OK;
+  if (env_flag("FA_TEST_FAIL_ALLOC")) return fail(FA_ERR_ALLOC, "device workspace (test hook)");
+  if (buf->ptr != nullptr) {
+    if (h->any_call) cudaEventSynchronize(h->last_call);
+    cudaFree(buf->ptr);
+    *buf = DeviceBuffer{};
+  }
+  const size_t want = align_up(bytes < 4096 ? 4096 : bytes, 4096);
+  const cudaError_t e = cudaMalloc(&buf->ptr, want);
+  if (e != cudaSuccess) {
+    buf->ptr = nullptr;
+    cudaGetLastError();
+    return fail(FA_ERR_ALLOC, "cudaMalloc(%zu): %s", want, cudaGetErrorString(e));
+  }
+  buf->bytes = want;
+  return FA_OK;
+}
+
+fa_status_t refuse_capture(cudaStream_t stream) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  if (cap != cudaStreamCaptureStatusNone)
+    return fail(FA_ERR_UNSUPPORTED, "this call cannot be captured into a graph");
+  return FA_OK;
+}
+
+void release_training(fa_handle_t h) {
+  for (DeviceBuffer* b : {&h->bwd.lists, &h->bwd.scratch, &h->rel.map, &h->rel.ext})
+    if (b->ptr) cudaFree(b->ptr);
+}
+
+fa_status_t validate_rel(const fa_desc_t* d, const fa_relbias_t* bias) {
+  if (!bias || !bias->table || !bias->bucket_of)
+    return fail(FA_ERR_NULLPTR, "the bias, its table and its bucket map are required");
+  if (d->alibi != FA_ALIBI_NONE)
+    return fail(FA_ERR_PARAM_INVALID, "the handle names an ALiBi variant, not a learned bias");
+  if (d->mask_kind != FA_MASK_NONE)
+    return fail(FA_ERR_UNSUPPORTED, "a relative position bias with an attenMask is not supported");
+  if (bias->reach < 1 || bias->num_buckets < 1)
+    return fail(FA_ERR_PARAM_INVALID, "reach and num_buckets must be >= 1 (got %d, %d)",
+                bias->reach, bias->num_buckets);
+  if (bias->reach > kRelMaxReach || bias->num_buckets > kRelMaxBuckets)
+    return fail(FA_ERR_UNSUPPORTED, "reach <= %d and num_buckets <= %d (got %d, %d)", kRelMaxReach,
+                kRelMaxBuckets, bias->reach, bias->num_buckets);
+  if ((uintptr_t)bias->table & 3u)
+    return fail(FA_ERR_PARAM_INVALID, "the bias table must be 4-byte aligned");
+  for (int32_t x = 0; x <= 2 * bias->reach; ++x)
+    if (bias->bucket_of[x] < 0 || bias->bucket_of[x] >= bias->num_buckets)
+      return fail(FA_ERR_PARAM_INVALID, "bucket_of[%d] = %d is outside [0, %d)", x,
+                  bias->bucket_of[x], bias->num_buckets);
+  return FA_OK;
+}
+
+fa_status_t prepare_rel(fa_handle_t h, const fa_relbias_t* bias, cudaStream_t stream,
+                        RelBias* out) {
+  const int32_t N = (int32_t)h->desc.N, R = bias->reach, row = rel_row(R);
+  if (h->any_call) {  // an earlier call on another stream may still read the tables
+    const cudaError_t e = cudaStreamWaitEvent(stream, h->last_call, 0);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
+  }
+  const size_t entries = (size_t)(2 * R + 1);
+  fa_status_t st = ensure_buffer(h, &h->rel.ext, (size_t)N * 4 * row * sizeof(float));
+  if (st != FA_OK) return st;
+  std::vector<int32_t>& held = h->rel.bucket_of;
+  if (held.size() != entries || !std::equal(held.begin(), held.end(), bias->bucket_of)) {
+    held.clear();
+    st = ensure_buffer(h, &h->rel.map, entries * sizeof(int32_t));
+    if (st != FA_OK) return st;
+    // Pageable memory: the call returns once the source has been read.
+    const cudaError_t e = cudaMemcpyAsync(h->rel.map.ptr, bias->bucket_of,
+                                          entries * sizeof(int32_t), cudaMemcpyHostToDevice, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyAsync(bucket map)");
+    held.assign(bias->bucket_of, bias->bucket_of + entries);
+  }
+  float* ext = static_cast<float*>(h->rel.ext.ptr);
+  const cudaError_t e = launch_rel_expand(bias->table, static_cast<const int32_t*>(h->rel.map.ptr),
+                                          ext, N, bias->num_buckets, R, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "bias expansion launch");
+  *out = RelBias{ext, R, row};
+  return FA_OK;
+}
+
+}  // namespace fa
+
+namespace {
+
+// Longest first, in buckets of similar length inside which the items of one
+// (sequence, head) stand together: the tiles in flight then share their
+// operands through L2 (see order_work_list).
+void order_items(std::vector<BwdItem>* items, bool locality) {
+  const int32_t bucket = locality ? kLocalityTiles : 1;
+  std::sort(items->begin(), items->end(), [bucket](const BwdItem& a, const BwdItem& c) {
+    const int32_t la = a.hi - a.lo, lc = c.hi - c.lo;
+    const int32_t ba = (la + bucket - 1) / bucket, bc = (lc + bucket - 1) / bucket;
+    if (ba != bc) return ba > bc;
+    if (a.b != c.b) return a.b < c.b;
+    if (a.h != c.h) return a.h < c.h;
+    if (la != lc) return la > lc;
+    return a.tile < c.tile;
+  });
+}
+
+// Builds and uploads the lists of this call's lengths unless the handle
+// holds them already.
+fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* cu_q,
+                          const int64_t* cu_kv, int has_mask, cudaStream_t stream) {
+  BwdState& bw = h->bwd;
+  std::vector<int64_t> key = make_key(&h->desc, prefix, cu_q, cu_kv, has_mask);
+  if (bw.valid && key == bw.key) return FA_OK;
+  const std::vector<SeqRec> recs = decode_geometry(&h->desc, prefix, cu_q, cu_kv, has_mask);
+  const int32_t N = (int32_t)h->desc.N;
+  int64_t tiles = 0, k_tiles = 0;
+  for (const SeqRec& s : recs) {
+    tiles += (s.sq + kTileM - 1) / kTileM;
+    k_tiles += (s.skv + kTileN - 1) / kTileN;
+  }
+  if (std::max(tiles, k_tiles) * N > 0x3fffffff)
+    return fail(FA_ERR_UNSUPPORTED, "too many work items");
+  std::vector<BwdItem> qi, ki;
+  qi.reserve((size_t)(tiles * N));
+  ki.reserve((size_t)(k_tiles * N));
+  int64_t base = 0;
+  for (size_t b = 0; b < recs.size(); ++b) {
+    const SeqRec& s = recs[b];
+    const int32_t nq = (s.sq + kTileM - 1) / kTileM, nk = (s.skv + kTileN - 1) / kTileN;
+    for (int32_t t = 0; t < nq; ++t) {
+      const TileRange r = tile_range(s, (int64_t)t * kTileM);
+      for (int32_t hd = 0; hd < N; ++hd)
+        qi.push_back(BwdItem{(int32_t)b, hd, t, (int32_t)(hd * tiles + base + t), r.lo, r.hi,
+                             r.full_lo, r.full_hi});
+    }
+    for (int32_t t = 0; t < nk; ++t) {
+      const TileRange r = key_tile_rows(s, (int64_t)t * kTileN);
+      for (int32_t hd = 0; hd < N; ++hd)
+        ki.push_back(BwdItem{(int32_t)b, hd, t, (int32_t)(hd * tiles + base), r.lo, r.hi, r.full_lo,
+                             r.full_hi});
+    }
+    base += nq;
+  }
+  order_items(&qi, claims_items((int64_t)qi.size(), h->num_sms));
+  order_items(&ki, claims_items((int64_t)ki.size(), h->num_sms));
+  const size_t seq_bytes = align_up(recs.size() * sizeof(SeqRec), 256);
+  const size_t q_bytes = align_up(qi.size() * sizeof(BwdItem), 256);
+  const size_t total = seq_bytes + q_bytes + ki.size() * sizeof(BwdItem);
+  bw.valid = false;
+  fa_status_t st = ensure_buffer(h, &bw.lists, total);
+  if (st != FA_OK) return st;
+  bw.host.assign(total, 0);
+  std::memcpy(bw.host.data(), recs.data(), recs.size() * sizeof(SeqRec));
+  if (!qi.empty()) std::memcpy(bw.host.data() + seq_bytes, qi.data(), qi.size() * sizeof(BwdItem));
+  if (!ki.empty())
+    std::memcpy(bw.host.data() + seq_bytes + q_bytes, ki.data(), ki.size() * sizeof(BwdItem));
+  // Pageable memory: the call returns once the source has been read.
+  const cudaError_t e =
+      cudaMemcpyAsync(bw.lists.ptr, bw.host.data(), total, cudaMemcpyHostToDevice, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyAsync(backward lists)");
+  bw.key.swap(key);
+  bw.valid = true;
+  bw.n_q = (int32_t)qi.size();
+  bw.n_k = (int32_t)ki.size();
+  bw.tiles = (int32_t)tiles;
+  bw.geo0 = recs.empty() ? SeqRec{} : recs[0];
+  return FA_OK;
+}
+
+struct BwdArgs {
+  const void *q, *k, *v;
+  const uint8_t* atten_mask;
+  const float* slopes;
+  const fa_relbias_t* bias;
+  const void* o;
+  const float* lse;
+  const void* d_o;
+  const float* d_lse;
+  const int64_t *prefix, *cu_q, *cu_kv;
+  void *dq, *dk, *dv;
+  float* dtable;
+};
+
+fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream) {
+  const fa_desc_t* d = &h->desc;
+  const bool rows = d->Sq > 0, keys = d->Skv > 0;
+  if (rows && (!a.q || !a.o || !a.lse || !a.d_o || !a.dq))
+    return fail(FA_ERR_NULLPTR, "q, o, lse, d_o and dq are required");
+  if (keys && (!a.k || !a.v || !a.dk || !a.dv))
+    return fail(FA_ERR_NULLPTR, "k, v, dk and dv are required");
+  const int has_mask = d->sparse_mode <= 1 && a.atten_mask != nullptr;
+  fa_status_t st = validate_call(d, a.prefix, a.cu_q, a.cu_kv, has_mask);
+  if (st != FA_OK) return st;
+  const uintptr_t align = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.o |
+                          (uintptr_t)a.d_o | (uintptr_t)a.dq | (uintptr_t)a.dk | (uintptr_t)a.dv;
+  if (align & 15u)
+    return fail(FA_ERR_PARAM_INVALID, "q, k, v, o, d_o, dq, dk and dv must be 16-byte aligned");
+  if (((uintptr_t)a.lse | (uintptr_t)a.d_lse | (uintptr_t)a.slopes | (uintptr_t)a.dtable) & 3u)
+    return fail(FA_ERR_PARAM_INVALID, "lse, d_lse, slopes and dtable must be 4-byte aligned");
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  st = refuse_capture(stream);
+  if (st != FA_OK) return st;
+  st = bind_device(h);
+  if (st != FA_OK) return st;
+  st = ensure_workspace(h, kHeaderBytes);  // the error word
+  if (st != FA_OK) return st;
+  cudaError_t e = cudaSuccess;
+  if (h->any_call) {  // lists and scratch are rewritten: order after the last call
+    e = cudaStreamWaitEvent(stream, h->last_call, 0);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
+  }
+  st = refresh_lists(h, a.prefix, a.cu_q, a.cu_kv, has_mask, stream);
+  if (st != FA_OK) return st;
+  const BwdState& bw = h->bwd;
+
+  // Scratch: row statistics | bias sums by tile and by distance | the dense
+  // mask's ranges and classes.
+  const size_t stat_bytes = align_up((size_t)bw.tiles * d->N * 256 * sizeof(float), 256);
+  const size_t W = a.bias ? 2 * (size_t)a.bias->reach + 1 : 0;
+  const size_t part_bytes = align_up((size_t)bw.tiles * d->N * W * sizeof(float), 256);
+  const size_t dist_bytes = align_up((size_t)d->N * W * sizeof(float), 256);
+  const int64_t planes = mask_planes(d, has_mask);
+  const size_t occ_bytes = planes ? occupancy_bytes(planes, d->Sq, d->Skv) : 0;
+  st = ensure_buffer(h, &h->bwd.scratch, stat_bytes + part_bytes + dist_bytes + occ_bytes);
+  if (st != FA_OK) return st;
+  uint8_t* scratch = static_cast<uint8_t*>(bw.scratch.ptr);
+  uint8_t* lists = static_cast<uint8_t*>(bw.lists.ptr);
+  const size_t seq_bytes = align_up((size_t)d->B * sizeof(SeqRec), 256);
+
+  BwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.seqs = reinterpret_cast<const SeqRec*>(lists);
+  BwdItem* q_items = reinterpret_cast<BwdItem*>(lists + seq_bytes);
+  BwdItem* k_items = reinterpret_cast<BwdItem*>(
+      lists + seq_bytes + align_up((size_t)bw.n_q * sizeof(BwdItem), 256));
+  p.q_items = q_items;
+  p.k_items = k_items;
+  p.n_q = bw.n_q;
+  p.n_k = bw.n_k;
+  p.stats = reinterpret_cast<float*>(scratch);
+  p.err_word = reinterpret_cast<unsigned int*>(h->d_ws);
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.o = a.o;
+  p.d_o = a.d_o;
+  p.lse = a.lse;
+  p.d_lse = a.d_lse;
+  p.dq = a.dq;
+  p.dk = a.dk;
+  p.dv = a.dv;
+  operand_strides(d, d->Sq, &p.q_sb, &p.q_sh, &p.q_st);
+  operand_strides(d, d->Skv, &p.k_sb, &p.k_sh, &p.k_st);
+  p.tnd = d->layout == FA_TND ? 1 : 0;
+  p.l_sb = p.tnd ? 0 : d->N * d->Sq;
+  p.l_sh = d->Sq;
+  p.scale = (float)d->scale;
+  p.scale_log2 = (float)(d->scale * 1.4426950408889634073599);
+  p.timeout_ns = h->timeout_ns;
+  if (d->alibi != FA_ALIBI_NONE) {
+    p.slopes = a.slopes;
+    p.alibi = d->alibi;
+  }
+  // An operand without elements is never loaded from: any valid address does.
+  const void* ops[4] = {a.q, a.k, a.v, a.d_o};
+  CUtensorMap* maps[4] = {&p.tm_q, &p.tm_k, &p.tm_v, &p.tm_do};
+  for (int i = 0; i < 4; ++i) {
+    const bool row_side = i == 0 || i == 3;
+    const int64_t S = row_side ? d->Sq : d->Skv;
+    const int64_t sb = row_side ? p.q_sb : p.k_sb, sh = row_side ? p.q_sh : p.k_sh,
+                  tok = row_side ? p.q_st : p.k_st;
+    const int64_t S1 = S > 0 ? S : 1;
+    if (!encode_operand_map(maps[i], S > 0 ? ops[i] : scratch, d->D, S, d->N, p.tnd ? 1 : d->B, tok,
+                            sh > 0 ? sh : d->D, p.tnd ? S1 * d->N * d->D : (sb > 0 ? sb : d->N * d->D)))
+      return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled failed for operand %d", i);
+  }
+  if (a.bias) {
+    st = prepare_rel(h, a.bias, stream, &p.rel);
+    if (st != FA_OK) return st;
+    p.rel_part = reinterpret_cast<float*>(scratch + stat_bytes);
+  }
+  if (has_mask) {
+    p.mask = a.atten_mask;
+    const int64_t plane = d->Sq * d->Skv;
+    p.m_si = d->Skv;
+    p.m_sb = d->mask_kind == FA_MASK_SS ? 0 : (d->mask_kind == FA_MASK_B1SS ? plane : d->N * plane);
+    p.m_sh = d->mask_kind == FA_MASK_BNSS ? plane : 0;
+    if (bw.n_q > 0 && bw.n_k > 0) {
+      OccParams oc;
+      std::memset(&oc, 0, sizeof(oc));
+      occupancy_shape(&oc, bw.geo0, planes);
+      oc.mask = a.atten_mask;
+      uint8_t* occ = scratch + stat_bytes + part_bytes + dist_bytes;
+      oc.ranges = reinterpret_cast<TileRange*>(occ);
+      oc.cls = occ + align_up((size_t)(oc.n_planes * oc.n_qt) * sizeof(TileRange), 256);
+      e = launch_occupancy(oc, h->num_sms, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "occupancy pre-pass launch");
+      BwdOccParams r;
+      std::memset(&r, 0, sizeof(r));
+      r.ranges = oc.ranges;
+      r.cls = oc.cls;
+      r.q_items = q_items;
+      r.k_items = k_items;
+      r.occ_sb = d->mask_kind == FA_MASK_SS ? 0 : (d->mask_kind == FA_MASK_B1SS ? 1 : d->N);
+      r.occ_sh = d->mask_kind == FA_MASK_BNSS ? 1 : 0;
+      r.n_q = bw.n_q;
+      r.n_k = bw.n_k;
+      r.n_qt = oc.n_qt;
+      r.n_kt = oc.n_kt;
+      e = launch_bwd_ranges(r, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "tile range launch");
+    }
+  }
+  e = launch_bwd_stats((int)d->D, p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "row statistics launch");
+  const char* why = nullptr;
+  e = launch_bwd((int)d->D, p, h->num_sms, stream, &why);
+  if (e != cudaSuccess) {
+    if (why) return fail(FA_ERR_UNSUPPORTED, "launch refused: %s", why);
+    return cuda_fail(e, "backward launch");
+  }
+  if (a.bias) {
+    e = launch_rel_reduce(p.rel_part, reinterpret_cast<float*>(scratch + stat_bytes + part_bytes),
+                          static_cast<const int32_t*>(h->rel.map.ptr), a.dtable, (int32_t)d->N,
+                          bw.tiles, a.bias->num_buckets, a.bias->reach, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "bias gradient launch");
+  }
+  e = cudaEventRecord(h->last_call, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
+  h->any_call = true;
+  return FA_OK;
+}
+
+// No C++ exception leaves a C entry point.
+fa_status_t backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream) {
+  try {
+    return enqueue_backward(h, a, cuda_stream);
+  } catch (const std::exception& e) {
+    return fail(FA_ERR_ALLOC, "host allocation: %s", e.what());
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status_t fa_bwd(fa_handle_t h, const void* q, const void* k, const void* v,
+                   const uint8_t* atten_mask, const void* o, const float* lse, const void* d_o,
+                   const float* d_lse, const int64_t* prefix, const int64_t* actual_seq_qlen,
+                   const int64_t* actual_seq_kvlen, void* dq, void* dk, void* dv,
+                   void* cuda_stream) {
+  clear_error();
+  if (!h) return fail(FA_ERR_NULLPTR, "handle is NULL");
+  if (h->desc.alibi != FA_ALIBI_NONE)
+    return fail(FA_ERR_PARAM_INVALID,
+                "the handle names an ALiBi variant: call fa_bwd_alibi with the slopes");
+  return backward(h, BwdArgs{q, k, v, atten_mask, nullptr, nullptr, o, lse, d_o, d_lse, prefix,
+                             actual_seq_qlen, actual_seq_kvlen, dq, dk, dv, nullptr},
+                  cuda_stream);
+}
+
+fa_status_t fa_bwd_alibi(fa_handle_t h, const void* q, const void* k, const void* v,
+                         const float* slopes, const void* o, const float* lse, const void* d_o,
+                         const float* d_lse, const int64_t* prefix, const int64_t* actual_seq_qlen,
+                         const int64_t* actual_seq_kvlen, void* dq, void* dk, void* dv,
+                         void* cuda_stream) {
+  clear_error();
+  if (!h) return fail(FA_ERR_NULLPTR, "handle is NULL");
+  if (!slopes) return fail(FA_ERR_NULLPTR, "slopes is NULL");
+  if (h->desc.alibi == FA_ALIBI_NONE)
+    return fail(FA_ERR_PARAM_INVALID, "fa_bwd_alibi needs a handle with an ALiBi variant");
+  return backward(h, BwdArgs{q, k, v, nullptr, slopes, nullptr, o, lse, d_o, d_lse, prefix,
+                             actual_seq_qlen, actual_seq_kvlen, dq, dk, dv, nullptr},
+                  cuda_stream);
+}
+
+fa_status_t fa_bwd_relbias(fa_handle_t h, const void* q, const void* k, const void* v,
+                           const fa_relbias_t* bias, const void* o, const float* lse,
+                           const void* d_o, const float* d_lse, const int64_t* prefix,
+                           const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
+                           void* dq, void* dk, void* dv, float* dtable, void* cuda_stream) {
+  clear_error();
+  if (!h) return fail(FA_ERR_NULLPTR, "handle is NULL");
+  fa_status_t st = validate_rel(&h->desc, bias);
+  if (st != FA_OK) return st;
+  if (!dtable) return fail(FA_ERR_NULLPTR, "dtable is NULL");
+  return backward(h, BwdArgs{q, k, v, nullptr, nullptr, bias, o, lse, d_o, d_lse, prefix,
+                             actual_seq_qlen, actual_seq_kvlen, dq, dk, dv, dtable},
+                  cuda_stream);
+}
+
+}  // extern "C"

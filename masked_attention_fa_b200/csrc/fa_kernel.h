@@ -15,6 +15,25 @@ enum : uint32_t {
   kErrWhereShift = 8u,   // bits 8..15: which wait gave up first (WaitSite)
 };
 
+// ------------------------------------------------- relative position bias
+// The bias of a pair depends on its head and on rel = j - (i + Skv - Sq)
+// alone: table[bucket_of[clip(rel, -reach, reach) + reach]][h]. Before each
+// call the table is laid out by distance, in log2 units: element x of head h
+// stands for the distance x - reach - kRelPad, so that a whole 128 x 128 tile
+// that holds a distance inside (-reach, reach) is read without clipping. Four
+// copies, copy s shifted by s elements, make every run of four distances one
+// aligned 16-byte load whatever its first distance.
+constexpr int kRelPad = 256;
+constexpr int kRelMaxReach = 1024;
+constexpr int kRelMaxBuckets = 4096;
+FA_HD int32_t rel_row(int32_t reach) { return (2 * reach + 1 + 2 * kRelPad + 3) / 4 * 4 + 4; }
+
+struct RelBias {
+  const float* ext;   // [N][4][rel_row(reach)], or null: no such bias
+  int32_t reach;
+  int32_t row;        // rel_row(reach)
+};
+
 // Kernel arguments (passed by value as a __grid_constant__ parameter; the
 // tensor maps must stay 64-byte aligned inside it).
 struct __align__(64) FwdParams {
@@ -45,6 +64,7 @@ struct __align__(64) FwdParams {
   // ALiBi (or null): per-head slopes [N], fp32; alibi is the fa_alibi_t
   // variant. Only the closed-form instances with item_tr add the bias.
   const float* slopes;
+  RelBias rel;             // the learned bias, by the same instances' rule
   int32_t alibi;
   int32_t n_items;
   int32_t tnd;             // packed tokens: TMA batch coordinate 0, token = offset + row

@@ -37,6 +37,9 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "fa_device.h"
 #include "fa_internal.h"
 #include "fa_kernel.h"
 #include "fa_tmem_asm.h"
@@ -100,6 +103,8 @@ constexpr int kRegsEpi = 64;
 constexpr int kRegsControl = 64;
 constexpr int kRegsTotal = 2 * 128 * kRegsSoftmax + 128 * kRegsEpi + 128 * kRegsControl;
 static_assert(kRegsTotal == kThreads * 128, "register split must equal the launch allocation");
+// What is added to the scores before the softmax.
+constexpr int kBiasNone = 0, kBiasAlibi = 1, kBiasRel = 2;
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the max grows by > 2^8
 
 // Where a wait gave up (error word bits 8..15).
@@ -167,76 +172,6 @@ struct Ctl {
 
 // ----------------------------------------------------------------- basics
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ uint64_t globaltimer_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 1/x and log2(x) on the exponential unit (one instruction each; relative
-// error a few ulp, far inside the tolerances of O and lse).
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2_fast(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// bf16x2 with `lo` in the low half (the even column of the pair).
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Three-input maximum (sm_100).
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// (a, b) <- (a, b) * m2 + c2, two lanes per instruction.
-__device__ __forceinline__ void fma_x2(float& a, float& b, uint64_t m2, uint64_t c2) {
-  asm("{\n\t.reg .b64 r;\n\t"
-      "mov.b64 r, {%0, %1};\n\t"
-      "fma.rn.f32x2 r, r, %2, %3;\n\t"
-      "mov.b64 {%0, %1}, r;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "l"(m2), "l"(c2));
-}
-
-// (a, b) += (x, y), two lanes per instruction.
-__device__ __forceinline__ void add_x2(float& a, float& b, float x, float y) {
-  asm("{\n\t.reg .b64 r, s;\n\t"
-      "mov.b64 r, {%0, %1};\n\t"
-      "mov.b64 s, {%2, %3};\n\t"
-      "add.rn.f32x2 r, r, s;\n\t"
-      "mov.b64 {%0, %1}, r;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "f"(x), "f"(y));
-}
-
 // 2^x for two values on the FMA pipe instead of the MUFU unit. Cody-Waite
 // reduction x = n + f with n = round(x) (adding 1.5 * 2^23 leaves n in the
 // low mantissa bits), a degree-3 minimax polynomial for 2^f on [-1/2, 1/2]
@@ -280,63 +215,6 @@ __device__ __forceinline__ float row_max128(const float (&x)[128]) {
   return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
 
-// ----------------------------------------------------------------- mbarrier
-
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
-               : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
-               "r"(bytes)
-               : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-struct WaitCtx {
-  volatile int* abort_flag;
-  unsigned int* err_word;
-  uint64_t timeout_ns;
-};
-
-// Wait for the phase with the given parity; false if the CTA is aborting or
-// the wait outlived the limit (then the error word records the site).
-// `honor_abort` = false is used by the drain waits of the abort path.
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, const WaitCtx& w,
-                                          uint32_t site, bool honor_abort = true) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t spin = 1;; ++spin) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((spin & 63u) == 0u) {
-      if (honor_abort && *w.abort_flag) return false;
-      if (globaltimer_ns() - t0 > w.timeout_ns) {
-        if (honor_abort) {
-          *w.abort_flag = 1;
-          atomicOr(w.err_word, kErrTimeout | (site << kErrWhereShift));
-        }
-        return false;
-      }
-    }
-  }
-}
-
 // Turn of softmax warpgroup s on the exponential unit: a hardware named
 // barrier (id 1 + s) over both warpgroups (256 threads). Warpgroup s waits
 // on it (bar.sync); the other warpgroup hands the turn over (bar.arrive)
@@ -377,13 +255,6 @@ __device__ __forceinline__ void turn_release(int s_other, const volatile int* ab
   if (__any_sync(0xffffffffu, *abort_flag != 0)) turn_pass(s_other, 0.f);
 }
 
-// Whole-warp wait: every lane waits, the warp proceeds only if all did.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& w,
-                                          uint32_t site) {
-  const bool ok = wait_bounded(bar, parity, w, site);
-  return __all_sync(0xffffffffu, ok);
-}
-
 // k-th item index of this CTA into the ring (TMA thread). The arrive
 // releases the store; the readers' wait acquires it.
 template <int NS>
@@ -418,73 +289,6 @@ __device__ __forceinline__ int idx_take_warp(Ctl<NS>* ctl, int k, const WaitCtx&
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl->idx_empty[slot]);
   return idx;
-}
-
-// ----------------------------------------------------------------- tcgen05
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// Shared-memory matrix descriptor, 128-byte swizzle (SM100 layout type 2,
-// descriptor version 1). Byte offsets lbo/sbo as the canonical layouts use:
-//   K-major:  rows 128 B apart, 8-row groups sbo = 1024 B apart (lbo unused);
-//   MN-major: 64-element MN blocks lbo apart, 8-row K groups sbo apart.
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// Instruction descriptor, kind::f16: bf16 x bf16 -> fp32, A K-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, bool b_mn_major) {
-  return (1u << 4)     // D format: f32
-         | (1u << 7)   // A format: bf16
-         | (1u << 10)  // B format: bf16
-         | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                       uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
-// Arrive on `bar` once every tcgen05.mma issued so far by this thread is done.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, uint64_t* bar,
-                                            int c0, int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
-      "r"(smem_u32(bar))
-      : "memory");
 }
 
 // ----------------------------------------------------------------- schedule
@@ -1032,43 +836,27 @@ __device__ __forceinline__ void apply_alibi(float (&x)[128], float scale_log2, f
   }
 }
 
+// Learned relative position bias: x <- x * scale_log2 + bias of the row's 128
+// keys, whose distances are consecutive: elements at .. at + 127 of the
+// head's biases by distance (log2 units), read as 16-byte loads from the copy
+// that is aligned for this row. Neighbouring rows read the same lines.
+__device__ __forceinline__ void apply_rel(float (&x)[128], float scale_log2, const float* ext,
+                                          int row, int at) {
+  const uint64_t s2 = pack_f32x2(scale_log2, scale_log2);
+  const float4* src = reinterpret_cast<const float4*>(ext + (int64_t)(at & 3) * row + (at & ~3));
+#pragma unroll
+  for (int c = 0; c < 128; c += 4) {
+    const float4 e = __ldg(src + c / 4);
+    fma_x2(x[c], x[c + 1], s2, pack_f32x2(e.x, e.y));
+    fma_x2(x[c + 2], x[c + 3], s2, pack_f32x2(e.z, e.w));
+  }
+}
+
 __device__ __forceinline__ float sum_acc(float (&acc)[8]) {
   add_x2(acc[0], acc[1], acc[2], acc[3]);
   add_x2(acc[4], acc[5], acc[6], acc[7]);
   add_x2(acc[0], acc[1], acc[4], acc[5]);
   return acc[0] + acc[1];
-}
-
-// O and lse stores that do not allocate in L1. The SM keeps only ~28 KB of
-// L1 beside 227 KB of shared memory; 64 KB of O per item written through it
-// evicts the work-item and sequence records every role reads at the next
-// item boundary (measured: +5 % causal, +2 % on the other workloads).
-__device__ __forceinline__ void st_global_na_v4(void* ptr, const uint4& v) {
-  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(ptr), "r"(v.x),
-               "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-// 32 bytes in one access (ptr 32-byte aligned): a row of O leaves the SM in
-// half as many accesses as with 16-byte stores. Each 16-byte store of the
-// epilogue's warp touches 32 rows, and the load/store unit is shared with
-// the softmax warps, whose shared-memory traffic (P) and item-boundary
-// accesses wait behind the epilogue's burst: measured +2 to +4 % on causal,
-// band and ALiBi, +1 % on the long-item workloads.
-__device__ __forceinline__ void st_global_na_v8(void* ptr, const uint4& a, const uint4& b) {
-  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                   ptr),
-               "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
-}
-__device__ __forceinline__ void st_global_na_f32(float* ptr, float v) {
-  asm volatile("st.global.L1::no_allocate.f32 [%0], %1;" ::"l"(ptr), "f"(v) : "memory");
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-               "r"(d)
-               : "memory");
 }
 
 // Row `row` of a 128 x 128 bf16 P tile at `base` (1024-byte aligned), in the
@@ -1111,12 +899,6 @@ __device__ __forceinline__ void exp_pack_store(const float (&x)[128], uint64_t m
   }
 }
 
-// Make this thread's generic-proxy shared-memory writes visible to the
-// tensor core's (async-proxy) reads that follow the next barrier.
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // Softmax of query sub-tile `sub` (one warpgroup, one row per thread). Per
 // key tile: read S_s, release it to the next QK, row maximum, then - in
 // strict alternation with the other softmax warpgroup, so that the two
@@ -1129,11 +911,14 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // warpgroup.
 // kDense: the dense-mask extras (the next mask line prefetched a tile ahead,
 // 16-byte mask gathers), compiled only into the dense-mask instance.
-// kAlibi: the ALiBi bias added to the scores before the row maximum.
-template <int D, bool kOcc, bool kDense, bool kClaim, bool kAlibi>
+// kBias: kBiasAlibi adds the ALiBi bias to the scores before the row maximum,
+// kBiasRel the learned relative position bias.
+template <int D, bool kOcc, bool kDense, bool kClaim, int kBias>
 __device__ void softmax_role(const FwdParams& p, Ctl<Cfg<D>::kStages>* ctl, float* inv_l_sm,
                              uint32_t tmem, uint8_t* sP, int sub, const WaitCtx& w) {
   using C = Cfg<D>;
+  constexpr bool kAlibi = kBias == kBiasAlibi;
+  constexpr bool kRel = kBias == kBiasRel;
   const int wq = (threadIdx.x >> 5) & 3;           // TMEM lane quarter of this warp
   const int lane = threadIdx.x & 31;
   const int row = wq * 32 + lane;                  // row of the sub-tile = TMEM lane
@@ -1193,6 +978,14 @@ __device__ void softmax_role(const FwdParams& p, Ctl<Cfg<D>::kStages>* ctl, floa
       slope = __ldg(p.slopes + it.h);
       a2 = slope * 1.4426950408889634f;
       dbase = -(i + (sr.skv - sr.sq));
+    }
+    // Learned bias: the head's biases by distance, and where the distance of
+    // key 0 from this row's diagonal sits in them.
+    const float* ext = nullptr;
+    int ext0 = 0;
+    if constexpr (kRel) {
+      ext = p.rel.ext + (int64_t)it.h * 4 * p.rel.row;
+      ext0 = p.rel.reach + kRelPad - (i + (sr.skv - sr.sq));
     }
     const uint8_t* mrow = nullptr;
     if ((sr.flags & kSeqDenseMask) && row_valid)
@@ -1285,7 +1078,22 @@ __device__ void softmax_role(const FwdParams& p, Ctl<Cfg<D>::kStages>* ctl, floa
       // Linear ALiBi: the tile's bias offset, a2 * (distance of its first key).
       const float abase = (kAlibi && p.alibi != 2) ? a2 * (float)(t * kTileN + dbase) : 0.f;
       if constexpr (kAlibi) apply_alibi(x, scale_log2, a2, t * kTileN + dbase, p.alibi == 2);
-      const float m_new = kAlibi ? row_max128(x) + abase : row_max128(x) * scale_log2;
+      float mul = kAlibi ? 1.f : scale_log2, base = abase;
+      if constexpr (kRel) {
+        // Distances of the tile's pairs: all at or below -reach, all at or
+        // above reach (one bias for the tile, a scalar like ALiBi's offset),
+        // or some between (a bias per key).
+        const int top = t * kTileN + kTileN - 1 - (int)(r0 + (sr.skv - sr.sq));
+        if (top <= -p.rel.reach) {
+          base = __ldg(ext);
+        } else if (top - (kTileM + kTileN - 2) >= p.rel.reach) {
+          base = __ldg(ext + p.rel.row - 1);
+        } else {
+          apply_rel(x, scale_log2, ext, p.rel.row, ext0 + t * kTileN);
+          mul = 1.f;
+        }
+      }
+      const float m_new = kBias ? fmaf(row_max128(x), mul, base) : row_max128(x) * scale_log2;
       const bool resc = m_new > m_used + kRescaleLog2;
       float alpha = 1.f;
       if (resc) {
@@ -1336,9 +1144,8 @@ __device__ void softmax_role(const FwdParams& p, Ctl<Cfg<D>::kStages>* ctl, floa
       if ((threadIdx.x & 127) == 0) FA_STAMP(sub, 4, turn - 1);
       FA_WSTAMP(0, turn - 1);
       const float ref = ((m_used == -INFINITY) ? 0.f : m_used) + zero;
-      const float mul = kAlibi ? 1.f : scale_log2;
       const uint64_t m2 = pack_f32x2(mul, mul);
-      const float off = kAlibi ? abase - ref : -ref;
+      const float off = kBias ? base - ref : -ref;
       const uint64_t c2 = pack_f32x2(off, off);
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if constexpr (kStoreInTurn) {
@@ -1493,9 +1300,10 @@ __device__ void epilogue_role(const FwdParams& p, Ctl<Cfg<D>::kStages>* ctl,
   }
 }
 
-template <int D, bool kOcc, bool kDense, bool kClaim, bool kAlibi>
+template <int D, bool kOcc, bool kDense, bool kClaim, int kBias>
 __global__ void __launch_bounds__(kThreads, 1) fa_fwd_sm100(const __grid_constant__ FwdParams p) {
   using C = Cfg<D>;
+  constexpr bool kAlibi = kBias == kBiasAlibi;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -1554,7 +1362,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_sm100(const __grid_constan
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_role<D, kOcc, kDense, kClaim, kAlibi>(p, ctl, inv_l_sm, tmem, sP, warp >> 2, w);
+    softmax_role<D, kOcc, kDense, kClaim, kBias>(p, ctl, inv_l_sm, tmem, sP, warp >> 2, w);
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     epilogue_role<D, kOcc, kClaim>(p, ctl, inv_l_sm, tmem, w);
@@ -1623,10 +1431,10 @@ bool encode_operand_map(CUtensorMap* tm, const void* base, int64_t D, int64_t S,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kOcc, bool kDense, bool kClaim = false, bool kAlibi = false>
+template <int D, bool kOcc, bool kDense, bool kClaim = false, int kBias = dev::kBiasNone>
 static cudaError_t launch_d(const FwdParams& p, int grid, cudaStream_t stream, const char** why) {
   using C = dev::Cfg<D>;
-  auto kern = dev::fa_fwd_sm100<D, kOcc, kDense, kClaim, kAlibi>;
+  auto kern = dev::fa_fwd_sm100<D, kOcc, kDense, kClaim, kBias>;
   static bool configured = false;
   static bool regs_ok = false;
   if (!configured) {
@@ -1651,36 +1459,34 @@ static cudaError_t launch_d(const FwdParams& p, int grid, cudaStream_t stream, c
 
 cudaError_t launch_fwd(int D, const FwdParams& p, int grid, cudaStream_t stream,
                        const char** why) {
-  // Six instances per head dim: ranges beside the items with the
+  // Eight instances per head dim: ranges beside the items with the
   // dense-mask extras, without them (fixed snake or claimed work, each also
-  // with the ALiBi bias), and ranges from the closed form (no item_tr). Only
-  // the claiming instances read p.claim.
+  // with the ALiBi bias or the learned bias), and ranges from the closed form
+  // (no item_tr). Only the claiming instances read p.claim.
   const bool occ = p.item_tr != nullptr;
   const bool dense = occ && p.mask != nullptr && p.m_si > 0;
   const bool claim = occ && !dense && p.claim != nullptr;
   const bool alibi = p.slopes != nullptr;
-  if (alibi && (!occ || dense)) {
-    if (why) *why = "an ALiBi bias needs a closed-form call with per-item ranges";
+  const bool rel = p.rel.ext != nullptr;
+  if ((alibi || rel) && (!occ || dense || (alibi && rel))) {
+    if (why) *why = "a bias needs a closed-form call with per-item ranges, and there is one at most";
     return cudaErrorInvalidValue;
   }
-  if (D == 128) {
+  auto pick = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
     if (alibi)
-      return claim ? launch_d<128, true, false, true, true>(p, grid, stream, why)
-                   : launch_d<128, true, false, false, true>(p, grid, stream, why);
-    return dense   ? launch_d<128, true, true>(p, grid, stream, why)
-           : claim ? launch_d<128, true, false, true>(p, grid, stream, why)
-           : occ   ? launch_d<128, true, false>(p, grid, stream, why)
-                   : launch_d<128, false, false>(p, grid, stream, why);
-  }
-  if (D == 64) {
-    if (alibi)
-      return claim ? launch_d<64, true, false, true, true>(p, grid, stream, why)
-                   : launch_d<64, true, false, false, true>(p, grid, stream, why);
-    return dense   ? launch_d<64, true, true>(p, grid, stream, why)
-           : claim ? launch_d<64, true, false, true>(p, grid, stream, why)
-           : occ   ? launch_d<64, true, false>(p, grid, stream, why)
-                   : launch_d<64, false, false>(p, grid, stream, why);
-  }
+      return claim ? launch_d<D, true, false, true, dev::kBiasAlibi>(p, grid, stream, why)
+                   : launch_d<D, true, false, false, dev::kBiasAlibi>(p, grid, stream, why);
+    if (rel)
+      return claim ? launch_d<D, true, false, true, dev::kBiasRel>(p, grid, stream, why)
+                   : launch_d<D, true, false, false, dev::kBiasRel>(p, grid, stream, why);
+    return dense   ? launch_d<D, true, true>(p, grid, stream, why)
+           : claim ? launch_d<D, true, false, true>(p, grid, stream, why)
+           : occ   ? launch_d<D, true, false>(p, grid, stream, why)
+                   : launch_d<D, false, false>(p, grid, stream, why);
+  };
+  if (D == 128) return pick(std::integral_constant<int, 128>{});
+  if (D == 64) return pick(std::integral_constant<int, 64>{});
   if (why) *why = "unsupported head dim";
   return cudaErrorInvalidValue;
 }
