@@ -56,6 +56,11 @@ FA_HD TileRange key_tile_rows(const SeqRec& s, int64_t c0) {
   return t;
 }
 
+// Sums of the bias's gradient by distance that a query tile writes: entry e
+// stands for the distance e - reach - kRelPad (a tile that holds a distance
+// inside (-reach, reach) reaches up to 254 past either end).
+FA_HD int32_t rel_width(int32_t reach) { return 2 * reach + 1 + 2 * kRelPad; }
+
 // Expand table [num_buckets][N] into ext.
 cudaError_t launch_rel_expand(const float* table, const int32_t* bucket_of, float* ext, int32_t N,
                               int32_t num_buckets, int32_t reach, cudaStream_t stream);
@@ -84,7 +89,7 @@ struct __align__(64) BwdParams {
   void* dv;
   const float* slopes;       // ALiBi, else null
   RelBias rel;
-  // Gradient of the bias by distance: one row of 2 reach + 1 sums per query
+  // Gradient of the bias by distance: one row of rel_width sums per query
   // tile (indexed by its statistics block), else null.
   float* rel_part;
   int64_t q_sb, q_sh, q_st;  // element strides of Q, O and their gradients
@@ -118,8 +123,8 @@ cudaError_t launch_bwd_ranges(const BwdOccParams& a, cudaStream_t stream);
 
 // dtable[c][h] = the sum of rel_part over head h's query tiles (rows
 // [h * tiles, (h + 1) * tiles) of rel_part) and the distances of bucket c, in
-// a fixed order. dist: scratch, fp32 [N][2 reach + 1].
-cudaError_t launch_rel_reduce(const float* rel_part, float* dist, const int32_t* bucket_of,
+// a fixed order. dist: scratch, fp64 [N][rel_width].
+cudaError_t launch_rel_reduce(const float* rel_part, double* dist, const int32_t* bucket_of,
                               float* dtable, int32_t N, int32_t tiles, int32_t num_buckets,
                               int32_t reach, cudaStream_t stream);
 

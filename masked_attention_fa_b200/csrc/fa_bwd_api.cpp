@@ -233,9 +233,9 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   // Scratch: row statistics | bias sums by tile and by distance | the dense
   // mask's ranges and classes.
   const size_t stat_bytes = align_up((size_t)bw.tiles * d->N * 256 * sizeof(float), 256);
-  const size_t W = a.bias ? 2 * (size_t)a.bias->reach + 1 : 0;
+  const size_t W = a.bias ? (size_t)rel_width(a.bias->reach) : 0;
   const size_t part_bytes = align_up((size_t)bw.tiles * d->N * W * sizeof(float), 256);
-  const size_t dist_bytes = align_up((size_t)d->N * W * sizeof(float), 256);
+  const size_t dist_bytes = align_up((size_t)d->N * W * sizeof(double), 256);
   const int64_t planes = mask_planes(d, has_mask);
   const size_t occ_bytes = planes ? occupancy_bytes(planes, d->Sq, d->Skv) : 0;
   st = ensure_buffer(h, &h->bwd.scratch, stat_bytes + part_bytes + dist_bytes + occ_bytes);
@@ -337,7 +337,7 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
     return cuda_fail(e, "backward launch");
   }
   if (a.bias) {
-    e = launch_rel_reduce(p.rel_part, reinterpret_cast<float*>(scratch + stat_bytes + part_bytes),
+    e = launch_rel_reduce(p.rel_part, reinterpret_cast<double*>(scratch + stat_bytes + part_bytes),
                           static_cast<const int32_t*>(h->rel.map.ptr), a.dtable, (int32_t)d->N,
                           bw.tiles, a.bias->num_buckets, a.bias->reach, stream);
     if (e != cudaSuccess) return cuda_fail(e, "bias gradient launch");

@@ -129,41 +129,42 @@ __global__ void __launch_bounds__(256) rel_expand(const float* __restrict__ tabl
   }
 }
 
-// First step: dist[h][d] = sum over head h's query tiles. One CTA per head
-// and 32 distances; warp w adds tiles w, w + 8, ... and the eight sums are
-// added in warp order.
+// First step: dist[h][e] = sum over head h's query tiles, in 64 bits. One CTA
+// per head and 32 distances; warp w adds tiles w, w + 8, ... and the eight
+// sums are added in warp order.
 __global__ void __launch_bounds__(256) rel_sum_tiles(const float* __restrict__ part,
-                                                     float* __restrict__ dist, int tiles, int W) {
-  __shared__ float sm[8][32];
+                                                     double* __restrict__ dist, int tiles, int W) {
+  __shared__ double sm[8][32];
   const int h = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = blockIdx.x * 32 + lane;
-  float s = 0.f;
+  double s = 0.0;
   if (d < W)
     for (int t = w; t < tiles; t += 8) s += part[((int64_t)h * tiles + t) * W + d];
   sm[w][lane] = s;
   __syncthreads();
   if (w == 0 && d < W) {
-    float a = sm[0][lane];
+    double a = sm[0][lane];
     for (int x = 1; x < 8; ++x) a += sm[x][lane];
     dist[(int64_t)h * W + d] = a;
   }
 }
 
-// Second step: one warp per (bucket, head) adds the distances of its bucket.
-__global__ void __launch_bounds__(256) rel_sum_buckets(const float* __restrict__ dist,
+// Second step: one warp per (bucket, head) adds the distances of its bucket,
+// those past the reach with the end they clip to.
+__global__ void __launch_bounds__(256) rel_sum_buckets(const double* __restrict__ dist,
                                                        const int32_t* __restrict__ bucket_of,
                                                        float* __restrict__ dtable, int N, int W,
-                                                       int num_buckets) {
+                                                       int reach, int num_buckets) {
   const int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (n >= (int64_t)num_buckets * N) return;
   const int c = (int)(n / N), h = (int)(n % N);
-  float s = 0.f;
-  for (int d = lane; d < W; d += 32)
-    if (bucket_of[d] == c) s += dist[(int64_t)h * W + d];
+  double s = 0.0;
+  for (int e = lane; e < W; e += 32)
+    if (bucket_of[min(max(e - kRelPad, 0), 2 * reach)] == c) s += dist[(int64_t)h * W + e];
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-  if (lane == 0) dtable[n] = s;
+  if (lane == 0) dtable[n] = (float)s;
 }
 
 }  // namespace
@@ -189,13 +190,13 @@ cudaError_t launch_rel_expand(const float* table, const int32_t* bucket_of, floa
   return cudaGetLastError();
 }
 
-cudaError_t launch_rel_reduce(const float* rel_part, float* dist, const int32_t* bucket_of,
+cudaError_t launch_rel_reduce(const float* rel_part, double* dist, const int32_t* bucket_of,
                               float* dtable, int32_t N, int32_t tiles, int32_t num_buckets,
                               int32_t reach, cudaStream_t stream) {
-  const int W = 2 * reach + 1;
+  const int W = rel_width(reach);
   rel_sum_tiles<<<dim3((W + 31) / 32, N), 256, 0, stream>>>(rel_part, dist, tiles, W);
   rel_sum_buckets<<<(int)(((int64_t)num_buckets * N + 7) / 8), 256, 0, stream>>>(
-      dist, bucket_of, dtable, N, W, num_buckets);
+      dist, bucket_of, dtable, N, W, reach, num_buckets);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,1011 @@
+// Masked attention backward for B200 (sm_100a), two kernels of one structure.
+//
+// With P = exp(score - lse) over the visible pairs and delta = sum dO o (see
+// fa_bwd.h for the row statistics):
+//     dV = P^T dO,   dS = P * (dO V^T - delta),   dQ = scale dS K,
+//     dK = scale dS^T Q
+// Neither P nor dS is written out: the query walk (kKeys = false) holds 128
+// query rows and visits their key tiles for dQ, the key walk (kKeys = true)
+// holds 128 keys and visits their query tiles for dK and dV. Each recomputes
+// the scores, so seven products run instead of five; in return every sum
+// stays in tensor memory and has one fixed order: no partial gradients go
+// through L2, no atomics, equal bits on every call.
+//
+// The walks are the same chain with the roles of the operands exchanged. A0,
+// A1 are held (Q, dO; K, V) and B0, B1 streamed (K, V; Q, dO):
+//     S = A0 B0^T, dP = A1 B1^T, acc0 += dS B0 (dQ; dK), acc1 += P B1 (dV)
+// The rows of every product are tensor memory lanes, and P and dS go back to
+// tensor memory in bf16, over the scores they came from, as the A operand of
+// the accumulating products: shared memory only feeds B (and, in the key
+// walk at head dim 128, where tensor memory is full, A0 and A1).
+//
+// One persistent CTA per SM, 16 warps:
+//   warps 0-7   P and dS; warps 0-3 columns 0..63 of a tile, 4-7 64..127
+//   warps 8-11  epilogue: accumulators to global memory; query walk: Q and
+//               dO of the next item from global to tensor memory
+//   warp 12     all MMAs (one thread; owns tensor memory)
+//   warp 13     TMA loads; clears the rows of a streamed tile that belong to
+//               the next packed sequence
+//   warp 14     idle
+//   warp 15     bias gradient: the tile's sums by distance (query walk)
+// MMA order per step: query walk S(t+1), dQ(t), dP(t+1); key walk dV(i),
+// S(i+1), dK(i), dP(i+1), also across items, so that the products of one
+// step run while P and dS of the other are computed.
+// Every mbarrier wait is bounded, as in the forward.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/fa.h"
+#include "fa_bwd.h"
+#include "fa_device.h"
+#include "fa_tmem_asm.h"
+
+namespace fa {
+namespace dev {
+
+constexpr int kBwdThreads = 512;
+// Register split over the 512 x 128 registers of the launch.
+constexpr int kBwdRegsMath = 168, kBwdRegsEpi = 112, kBwdRegsControl = 64;
+static_assert(256 * kBwdRegsMath + 128 * kBwdRegsEpi + 128 * kBwdRegsControl == kBwdThreads * 128,
+              "register split must equal the launch allocation");
+constexpr int kBwdBiasNone = 0, kBwdBiasAlibi = 1, kBwdBiasRel = 2;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Where a wait gave up (error word bits 8..15), after the forward's sites.
+enum BwdSite : uint32_t {
+  kBSiteB0Empty = 32, kBSiteB1Empty, kBSiteStatEmpty, kBSiteA0Empty, kBSiteA1Empty, kBSiteFix,
+  kBSiteB0Full, kBSiteB1Full, kBSiteStatFull, kBSiteA0Full, kBSiteA1Full, kBSiteSFull, kBSiteSFree,
+  kBSitePFull, kBSiteDpFull, kBSiteDsFull, kBSiteAccFull, kBSiteAccFree, kBSiteSumFull,
+  kBSiteSumEmpty, kBSiteFarFull, kBSiteFarEmpty, kBSiteDrain, kBSiteSmem,
+};
+
+template <int D, bool kKeys>
+struct BCfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr uint32_t kChunkBytes = 128u * 128u;
+  static constexpr uint32_t kTileBytes = 128u * D * 2u;
+  // Ring depths. B0(t) is read first by S(t) and last by acc0(t), a step
+  // later; B1(t) by dP(t) (and acc1(t)).
+  static constexpr int kN0 = (D == 128 && kKeys) ? 3 : 4;
+  static constexpr int kN1 = D == 128 ? 2 : 4;
+  static constexpr uint32_t kABytes = kKeys ? 2u * kTileBytes : 0u;
+  static constexpr uint32_t kRingBytes = (kN0 + kN1) * kTileBytes;
+  static constexpr uint32_t kStatBytes = kKeys ? 2u * 1024u : 0u;
+  static constexpr uint32_t kSumBytes = kKeys ? 0u : 2u * 8u * 96u * 4u;
+  static constexpr uint32_t kCtlBytes = 1024u;
+  static constexpr uint32_t kSmemBytes = kABytes + kRingBytes + kStatBytes + kSumBytes + kCtlBytes;
+  static_assert(kSmemBytes <= 227u * 1024u, "shared memory budget");
+  // Tensor memory columns.
+  static constexpr uint32_t kColS = 0, kColDP = 128, kColAcc0 = 256, kColAcc1 = 256 + D;
+  static constexpr uint32_t kColA0 = 256 + D, kColA1 = 256 + D + D / 2;  // query walk
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kColAcc1 + D <= kTmemCols && kColA1 + D / 2 <= kTmemCols, "tensor memory budget");
+};
+
+struct BCtl {
+  uint64_t b0_full[4], b0_empty[4], b1_full[4], b1_empty[4];
+  uint64_t stat_full[2], stat_empty[2];  // key walk: the query tile's row statistics
+  uint64_t fix;                          // a tile whose tail the load warp clears
+  uint64_t a0_full, a0_empty, a1_full, a1_empty;
+  uint64_t s_full, s_free;   // S in tensor memory / read into registers (query walk)
+  uint64_t p_full;           // P in tensor memory (key walk)
+  uint64_t dp_full, ds_full;
+  uint64_t acc_full[2], acc_free[2];
+  uint64_t sum_full[2], sum_empty[2];    // bias gradient: sums by diagonal of one tile
+  uint64_t far_full, far_empty;          // ... and of the tiles past the reach
+  uint64_t drain;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  float far[8][2];
+};
+static_assert(sizeof(BCtl) <= 1024, "barrier area");
+
+// (a, b) <- (a, b) * (x, y), two lanes per instruction.
+__device__ __forceinline__ void mul_x2(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 r, s;\n\t"
+      "mov.b64 r, {%0, %1};\n\t"
+      "mov.b64 s, {%2, %3};\n\t"
+      "mul.rn.f32x2 r, r, s;\n\t"
+      "mov.b64 {%0, %1}, r;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// k-th item of this CTA: the lists are in descending order of length and
+// dealt out in a snake, which evens out the per-CTA sums.
+__device__ __forceinline__ int bwd_item(int k) {
+  const int G = gridDim.x, c = blockIdx.x;
+  return k * G + ((k & 1) ? (G - 1 - c) : c);
+}
+
+// The CTA's steps in order: tile t of an item that has tiles.
+struct Step {
+  int k;        // next position of the CTA's list
+  int t, lo, hi;
+  bool valid, first, last;
+};
+
+__device__ __forceinline__ void next_step(const BwdItem* items, int n, Step& s) {
+  if (s.valid && s.t + 1 < s.hi) {
+    ++s.t;
+    s.first = false;
+    s.last = s.t + 1 == s.hi;
+    return;
+  }
+  for (;;) {
+    const int idx = bwd_item(s.k);
+    if (idx >= n) {
+      s.valid = false;
+      return;
+    }
+    ++s.k;
+    const int4 r = __ldg(reinterpret_cast<const int4*>(items + idx) + 1);  // lo, hi, full range
+    if (r.y <= r.x) continue;
+    s.t = s.lo = r.x;
+    s.hi = r.y;
+    s.valid = s.first = true;
+    s.last = s.t + 1 == s.hi;
+    return;
+  }
+}
+
+// ----------------------------------------------------------------- roles
+
+// TMA loads (a whole warp; lane 0 issues): per step the tile of B0, the row
+// statistics (key walk) and the tile of B1; in the key walk the item's K and
+// V follow its first tiles, as soon as the previous item has read its own.
+template <int D, bool kKeys>
+__device__ void bwd_load(const BwdParams& p, BCtl* ctl, uint8_t* sA, uint8_t* sB0, uint8_t* sB1,
+                         uint8_t* sStat, const WaitCtx& w) {
+  using C = BCfg<D, kKeys>;
+  const int lane = threadIdx.x & 31;
+  const BwdItem* items = kKeys ? p.k_items : p.q_items;
+  const int n_items = kKeys ? p.n_k : p.n_q;
+  const CUtensorMap* tm0 = kKeys ? &p.tm_q : &p.tm_k;
+  const CUtensorMap* tm1 = kKeys ? &p.tm_do : &p.tm_v;
+  uint32_t n0 = 0, n1 = 0, ns = 0, na0 = 0, na1 = 0, nfix = 0;
+  bool ok = true, fixing = false;
+  auto tma_tile = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int row, int h, int bc) {
+    mbar_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+    for (int c = 0; c < C::kChunks; ++c)
+      tma_load_4d(dst + c * C::kChunkBytes, tm, bar, c * 64, row, h, bc);
+  };
+  // One streamed tile of which `rows` rows belong to the sequence. Rows past
+  // a packed sequence's end are another sequence's tokens: they are cleared,
+  // so that a zero weight times whatever they hold adds nothing.
+  auto load_b = [&](uint8_t* ring, uint64_t* full, uint64_t* empty, uint32_t& n, int slots,
+                    const CUtensorMap* tm, int row, int rows, int h, int bc, uint32_t site) -> bool {
+    const uint32_t st = n % slots;
+    if (n >= (uint32_t)slots && !wait_warp(&empty[st], ((n / slots) - 1) & 1u, w, site))
+      return false;
+    uint8_t* dst = ring + st * C::kTileBytes;
+    const bool clear = p.tnd && rows < 128;
+    if (lane == 0) tma_tile(dst, tm, clear ? &ctl->fix : &full[st], row, h, bc);
+    __syncwarp();
+    if (clear) {
+      // The copy is complete before anything is written over its rows.
+      fixing = true;
+      if (!wait_warp(&ctl->fix, nfix & 1u, w, kBSiteFix)) return false;
+      fixing = false;
+      ++nfix;
+      for (int x = rows * 8 + lane; x < 128 * 8; x += 32)
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+          st_shared_v4(smem_u32(dst) + c * C::kChunkBytes + x * 16, 0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
+    }
+    ++n;
+    return true;
+  };
+  for (int k = 0; ok; ++k) {
+    const int idx = bwd_item(k);
+    if (idx >= n_items) break;
+    const BwdItem it = items[idx];
+    if (it.hi <= it.lo) continue;
+    const SeqRec sr = p.seqs[it.b];
+    const int bc = p.tnd ? 0 : it.b;
+    const int off = kKeys ? sr.q_off : sr.kv_off, len = kKeys ? sr.sq : sr.skv;
+    for (int t = it.lo; t < it.hi && ok; ++t) {
+      const int row = off + t * 128, rows = min(128, len - t * 128);
+      ok = load_b(sB0, ctl->b0_full, ctl->b0_empty, n0, C::kN0, tm0, row, rows, it.h, bc,
+                  kBSiteB0Empty);
+      if (kKeys && ok && t == it.lo) {
+        ok = na0 == 0 || wait_warp(&ctl->a0_empty, (na0 - 1) & 1u, w, kBSiteA0Empty);
+        if (ok && lane == 0)
+          tma_tile(sA, &p.tm_k, &ctl->a0_full, sr.kv_off + it.tile * 128, it.h, bc);
+        if (ok) ++na0;
+      }
+      if (kKeys && ok) {
+        const uint32_t st = ns & 1u;
+        ok = ns < 2 || wait_warp(&ctl->stat_empty[st], ((ns >> 1) - 1) & 1u, w, kBSiteStatEmpty);
+        if (ok && lane == 0) {
+          mbar_expect_tx(&ctl->stat_full[st], 1024u);
+          bulk_load(sStat + st * 1024u, p.stats + ((int64_t)it.stat + t) * 256, 1024u,
+                    &ctl->stat_full[st]);
+        }
+        if (ok) ++ns;
+      }
+      if (ok)
+        ok = load_b(sB1, ctl->b1_full, ctl->b1_empty, n1, C::kN1, tm1, row, rows, it.h, bc,
+                    kBSiteB1Empty);
+      if (kKeys && ok && t == it.lo) {
+        ok = na1 == 0 || wait_warp(&ctl->a1_empty, (na1 - 1) & 1u, w, kBSiteA1Empty);
+        if (ok && lane == 0)
+          tma_tile(sA + C::kTileBytes, &p.tm_v, &ctl->a1_full, sr.kv_off + it.tile * 128, it.h, bc);
+        if (ok) ++na1;
+      }
+    }
+  }
+  if (!ok && lane == 0) {
+    // Abort: let every copy this warp started land before the CTA exits.
+    if (fixing) wait_bounded(&ctl->fix, nfix & 1u, w, kBSiteDrain, false);
+    for (uint32_t r = n0 > (uint32_t)C::kN0 ? n0 - C::kN0 : 0u; r < n0; ++r)
+      wait_bounded(&ctl->b0_full[r % C::kN0], (r / C::kN0) & 1u, w, kBSiteDrain, false);
+    for (uint32_t r = n1 > (uint32_t)C::kN1 ? n1 - C::kN1 : 0u; r < n1; ++r)
+      wait_bounded(&ctl->b1_full[r % C::kN1], (r / C::kN1) & 1u, w, kBSiteDrain, false);
+    for (uint32_t r = ns > 2u ? ns - 2u : 0u; r < ns; ++r)
+      wait_bounded(&ctl->stat_full[r & 1u], (r >> 1) & 1u, w, kBSiteDrain, false);
+    if (na0) wait_bounded(&ctl->a0_full, (na0 - 1) & 1u, w, kBSiteDrain, false);
+    if (na1) wait_bounded(&ctl->a1_full, (na1 - 1) & 1u, w, kBSiteDrain, false);
+  }
+  __syncwarp();
+}
+
+// D[128 x 128] = A B^T, both K-major over the head dim; A in shared memory
+// (key walk) or tensor memory.
+template <int D, bool kKeys>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a_tmem, const uint8_t* a_smem,
+                                             const uint8_t* b_smem) {
+  using C = BCfg<D, kKeys>;
+  constexpr uint32_t idesc = idesc_bf16(128, 128, false);
+  const uint64_t b0 = sdesc(smem_u32(b_smem), 16u, 1024u);
+  const uint64_t a0 = sdesc(smem_u32(a_smem), 16u, 1024u);
+#pragma unroll 1
+  for (int k = 0; k < D / 16; ++k) {
+    const uint64_t off = (uint64_t)(((k >> 2) * C::kChunkBytes + (k & 3) * 32u) >> 4);
+    if constexpr (kKeys) mma_ss(d, a0 + off, b0 + off, idesc, k > 0 ? 1u : 0u);
+    else mma_ts(d, a_tmem + k * 8u, b0 + off, idesc, k > 0 ? 1u : 0u);
+  }
+}
+
+// acc[128 x D] += W B with W (P or dS, bf16) in tensor memory: columns
+// 0..63 in the first 32 tensor memory columns from `a`, 64..127 from a + 64.
+template <int D, bool kKeys>
+__device__ __forceinline__ void issue_acc(uint32_t d, uint32_t a, const uint8_t* b_smem,
+                                          bool accumulate) {
+  using C = BCfg<D, kKeys>;
+  constexpr uint32_t idesc = idesc_bf16(128, D, true);
+  const uint64_t b0 = sdesc(smem_u32(b_smem), C::kChunkBytes, 1024u);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    mma_ts(d, a + (k >> 2) * 64u + (k & 3) * 8u, b0 + (uint64_t)(k * (2048u >> 4)), idesc,
+           (accumulate || k > 0) ? 1u : 0u);
+}
+
+// All products (one thread). The products that overwrite tensor memory which
+// an earlier product still reads are issued after it by this same thread:
+// products execute in order.
+template <int D, bool kKeys>
+__device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint8_t* sA,
+                        const uint8_t* sB0, const uint8_t* sB1, const WaitCtx& w) {
+  using C = BCfg<D, kKeys>;
+  const BwdItem* items = kKeys ? p.k_items : p.q_items;
+  const int n_items = kKeys ? p.n_k : p.n_q;
+  const uint32_t tS = tmem + C::kColS, tDP = tmem + C::kColDP;
+  Step cur, nx;
+  nx.k = 0;
+  nx.valid = false;
+  next_step(items, n_items, nx);
+  uint32_t n = 0;       // step of nx
+  uint32_t a0 = 0, a1 = 0;  // held operands awaited
+  uint32_t items_done = 0;
+  auto scores = [&]() -> bool {
+    if (nx.first && !wait_bounded(&ctl->a0_full, a0++ & 1u, w, kBSiteA0Full)) return false;
+    const uint32_t st = n % C::kN0;
+    if (!wait_bounded(&ctl->b0_full[st], (n / C::kN0) & 1u, w, kBSiteB0Full)) return false;
+    if (!kKeys && n > 0 && !wait_bounded(&ctl->s_free, (n - 1) & 1u, w, kBSiteSFree)) return false;
+    tc_fence_after();
+    issue_scores<D, kKeys>(tS, tmem + C::kColA0, sA, sB0 + st * C::kTileBytes);
+    mma_commit(&ctl->s_full);
+    if (nx.last) mma_commit(&ctl->a0_empty);
+    return true;
+  };
+  auto dprobs = [&]() -> bool {
+    if (nx.first && !wait_bounded(&ctl->a1_full, a1++ & 1u, w, kBSiteA1Full)) return false;
+    const uint32_t st = n % C::kN1;
+    if (!wait_bounded(&ctl->b1_full[st], (n / C::kN1) & 1u, w, kBSiteB1Full)) return false;
+    tc_fence_after();
+    issue_scores<D, kKeys>(tDP, tmem + C::kColA1, sA + C::kTileBytes, sB1 + st * C::kTileBytes);
+    mma_commit(&ctl->dp_full);
+    if (!kKeys) mma_commit(&ctl->b1_empty[st]);
+    if (nx.last) mma_commit(&ctl->a1_empty);
+    return true;
+  };
+  bool ok = !nx.valid || (scores() && dprobs());
+  while (ok && nx.valid) {
+    cur = nx;
+    const uint32_t c = n;
+    next_step(items, n_items, nx);
+    ++n;
+    if constexpr (kKeys) {
+      if (!wait_bounded(&ctl->p_full, c & 1u, w, kBSitePFull)) break;
+      if (cur.first && items_done > 0 &&
+          !wait_bounded(&ctl->acc_free[1], (items_done - 1) & 1u, w, kBSiteAccFree))
+        break;
+      tc_fence_after();
+      const uint32_t st = c % C::kN1;
+      issue_acc<D, kKeys>(tmem + C::kColAcc1, tS, sB1 + st * C::kTileBytes, !cur.first);
+      mma_commit(&ctl->b1_empty[st]);
+      if (cur.last) mma_commit(&ctl->acc_full[1]);
+    }
+    if (nx.valid && !scores()) break;
+    if (!wait_bounded(&ctl->ds_full, c & 1u, w, kBSiteDsFull)) break;
+    if (cur.first && items_done > 0 &&
+        !wait_bounded(&ctl->acc_free[0], (items_done - 1) & 1u, w, kBSiteAccFree))
+      break;
+    tc_fence_after();
+    const uint32_t st = c % C::kN0;
+    issue_acc<D, kKeys>(tmem + C::kColAcc0, tDP, sB0 + st * C::kTileBytes, !cur.first);
+    mma_commit(&ctl->b0_empty[st]);
+    if (cur.last) {
+      mma_commit(&ctl->acc_full[0]);
+      ++items_done;
+    }
+    if (nx.valid && !dprobs()) break;
+  }
+  // Wait until every MMA this thread issued (and its commits) has finished
+  // with tensor and shared memory.
+  mma_commit(&ctl->drain);
+  wait_bounded(&ctl->drain, 0u, w, kBSiteDrain, false);
+}
+
+// One bit per column of [0, 64): inside [lo, hi].
+__device__ __forceinline__ void interval_bits(int lo, int hi, uint32_t (&wm)[2]) {
+#pragma unroll
+  for (int wd = 0; wd < 2; ++wd) {
+    const int a = lo - 32 * wd, b = hi - 32 * wd;
+    const uint32_t upto = b >= 31 ? 0xffffffffu : (b < 0 ? 0u : (0xffffffffu >> (31 - b)));
+    const uint32_t from = a <= 0 ? 0xffffffffu : (a > 31 ? 0u : (0xffffffffu << a));
+    wm[wd] = upto & from;
+  }
+}
+
+// P and dS of one half (64 columns) of every tile, one row per thread. Per
+// step: S to registers, P = 2^(scale log2e S + bias - lse log2e) (masked
+// entries 0), in the key walk P back in bf16 over S; then dP to registers,
+// dS = P (dP - delta) back in bf16 over dP. P is rounded to bf16 only as an
+// operand of dV; dS uses the fp32 value.
+template <int D, bool kKeys, int kBias>
+__device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint8_t* sStat,
+                         float* sSum, const WaitCtx& w) {
+  using C = BCfg<D, kKeys>;
+  constexpr bool kRel = kBias == kBwdBiasRel;
+  constexpr bool kGrad = kRel && !kKeys;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wq = warp & 3, g = warp >> 2;
+  const int row = wq * 32 + lane;
+  const uint32_t lane_bits = (uint32_t)(wq * 32) << 16;
+  const uint32_t tS = tmem + lane_bits + C::kColS + 64u * g;
+  const uint32_t tDP = tmem + lane_bits + C::kColDP + 64u * g;
+  const BwdItem* items = kKeys ? p.k_items : p.q_items;
+  const int n_items = kKeys ? p.n_k : p.n_q;
+  const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
+  uint32_t n = 0;      // steps
+  uint32_t n_near = 0, n_far = 0;
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const int idx = bwd_item(k);
+    if (idx >= n_items) break;
+    const BwdItem it = items[idx];
+    if (it.hi <= it.lo) continue;
+    const SeqRec sr = p.seqs[it.b];
+    const int delta = sr.skv - sr.sq;
+    const int at = it.tile * 128 + row;  // this thread's query row or key
+    const bool stored = at < (kKeys ? sr.skv : sr.sq);
+    // Visible columns of this row: keys of a query row, or query rows of a key.
+    int v_lo = 1, v_hi = 0;
+    if (stored) {
+      if constexpr (kKeys) {
+        v_lo = at < sr.prefix ? 0 : (int)imin64(imax64(0, (int64_t)at - sr.hi_off), sr.sq);
+        v_hi = (int)imax64(imin64(sr.sq - 1, (int64_t)at - sr.lo_off), -1);
+      } else {
+        v_lo = (int)imin64(imax64(0, row_lo(sr, at)), sr.skv);
+        v_hi = (int)imax64(imin64(sr.skv - 1, row_hi(sr, at)), -1);
+      }
+    }
+    const uint8_t* mrow = nullptr;  // the mask from this row's entry of column 0
+    int64_t m_step = 0;
+    if ((sr.flags & kSeqDenseMask) && stored) {
+      mrow = p.mask + it.b * p.m_sb + it.h * p.m_sh + (kKeys ? at : at * p.m_si);
+      m_step = kKeys ? p.m_si : 1;
+    }
+    float nl = 0.f, nd = 0.f;
+    if constexpr (!kKeys) {
+      nl = __ldg(p.stats + (int64_t)it.stat * 256 + row);
+      nd = __ldg(p.stats + (int64_t)it.stat * 256 + 128 + row);
+    }
+    float a2 = 0.f;
+    if constexpr (kBias == kBwdBiasAlibi) a2 = __ldg(p.slopes + it.h) * kLog2e;
+    const float* ext = nullptr;
+    if constexpr (kRel) ext = p.rel.ext + (int64_t)it.h * 4 * p.rel.row;
+    float far_lo = 0.f, far_hi = 0.f;
+
+    for (int t = it.lo; t < it.hi; ++t, ++n) {
+      const bool partial = !(t >= it.full_lo && t < it.full_hi);
+      const int c0 = t * 128 + 64 * g;  // first column of this half
+      // Distance key - diagonal of the row's column 0; it grows with the
+      // column in the query walk and falls with it in the key walk.
+      const int rel0 = kKeys ? at - (c0 + delta) : c0 - (at + delta);
+      uint32_t wm[2] = {0xffffffffu, 0xffffffffu};
+      if (partial) {
+        interval_bits(v_lo - c0, v_hi - c0, wm);
+        if (mrow != nullptr) {
+          const uint8_t* mt = mrow + c0 * m_step;
+#pragma unroll
+          for (int wd = 0; wd < 2; ++wd) {
+            uint32_t see = wm[wd], hide = 0u;
+#pragma unroll 8
+            for (int c = 0; c < 32; ++c)
+              if (((see >> c) & 1u) && __ldg(mt + (wd * 32 + c) * m_step) != 0) hide |= 1u << c;
+            wm[wd] = see & ~hide;
+          }
+        }
+      }
+      const float* st = reinterpret_cast<const float*>(sStat + (n & 1u) * 1024u) + 64 * g;
+      if (kKeys && !wait_warp(&ctl->stat_full[n & 1u], (n >> 1) & 1u, w, kBSiteStatFull)) {
+        ok = false;
+        break;
+      }
+      if (!wait_warp(&ctl->s_full, n & 1u, w, kBSiteSFull)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float x[64];
+      {
+        uint32_t sv[64];
+        tmem_ld64_wait(tS, sv);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(sv[c]);
+      }
+      if constexpr (!kKeys) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->s_free);
+      }
+      // Exponent: scale log2e S + bias - lse log2e.
+      // Learned bias: past the reach on one side in the whole tile (one
+      // scalar), or a bias per distance.
+      float base = 0.f;
+      bool near = false;
+      if constexpr (kRel) {
+        const int top = kKeys ? it.tile * 128 + 127 - (t * 128 + delta)
+                              : t * 128 + 127 - (it.tile * 128 + delta);
+        near = !(top <= -p.rel.reach || top - 254 >= p.rel.reach);
+        if (!near) base = __ldg(top <= -p.rel.reach ? ext : ext + p.rel.row - 1);
+      }
+      if constexpr (kBias == kBwdBiasAlibi) {
+        const float d0 = (float)rel0;
+        constexpr float kSign = kKeys ? -1.f : 1.f;
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float da = d0, db = d0;
+          add_x2(da, db, kSign * c, kSign * (c + 1));
+          if (p.alibi == FA_ALIBI_SQRT) {
+            float ra, rb;
+            asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(ra) : "f"(fabsf(da)));
+            asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(rb) : "f"(fabsf(db)));
+            da = copysignf(ra, da);
+            db = copysignf(rb, db);
+          }
+          const float la = kKeys ? st[c] : nl, lb = kKeys ? st[c + 1] : nl;
+          fma_x2(da, db, pack_f32x2(a2, a2), pack_f32x2(la, lb));
+          fma_x2(x[c], x[c + 1], scale2, pack_f32x2(da, db));
+        }
+      } else if (kRel && near) {
+        // ext entry of column 0, and the copy in which four consecutive
+        // distances of these columns are one aligned 16-byte load.
+        const int e0 = rel0 + p.rel.reach + kRelPad;
+        const int first = kKeys ? e0 - 3 : e0;
+        const float4* src =
+            reinterpret_cast<const float4*>(ext + (int64_t)(first & 3) * p.rel.row + (first & ~3));
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          float4 e = __ldg(kKeys ? src - c / 4 : src + c / 4);
+          if (kKeys) e = make_float4(e.w, e.z, e.y, e.x);
+          if constexpr (kKeys) {
+            const float4 l = *reinterpret_cast<const float4*>(st + c);
+            add_x2(e.x, e.y, l.x, l.y);
+            add_x2(e.z, e.w, l.z, l.w);
+          } else {
+            add_x2(e.x, e.y, nl, nl);
+            add_x2(e.z, e.w, nl, nl);
+          }
+          fma_x2(x[c], x[c + 1], scale2, pack_f32x2(e.x, e.y));
+          fma_x2(x[c + 2], x[c + 3], scale2, pack_f32x2(e.z, e.w));
+        }
+      } else {
+        const uint64_t l2 = pack_f32x2(nl + base, nl + base);
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          if constexpr (kKeys) {
+            float4 l = *reinterpret_cast<const float4*>(st + c);
+            if constexpr (kRel) {
+              add_x2(l.x, l.y, base, base);
+              add_x2(l.z, l.w, base, base);
+            }
+            fma_x2(x[c], x[c + 1], scale2, pack_f32x2(l.x, l.y));
+            fma_x2(x[c + 2], x[c + 3], scale2, pack_f32x2(l.z, l.w));
+          } else {
+            fma_x2(x[c], x[c + 1], scale2, l2);
+            fma_x2(x[c + 2], x[c + 3], scale2, l2);
+          }
+        }
+      }
+      if (partial) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          x[c] = ((wm[c >> 5] >> (c & 31)) & 1u) ? x[c] : -INFINITY;
+      }
+#pragma unroll
+      for (int c = 0; c < 64; ++c) x[c] = ex2(x[c]);
+      if constexpr (kKeys) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
+        tmem_st32(tS, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_full);
+      }
+      if (!wait_warp(&ctl->dp_full, n & 1u, w, kBSiteDpFull)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      {
+        uint32_t dv[64];
+        tmem_ld64_wait(tDP, dv);
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          float y[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[q] = __uint_as_float(dv[c + q]);
+          if constexpr (kKeys) {
+            const float4 l = *reinterpret_cast<const float4*>(st + 128 + c);
+            add_x2(y[0], y[1], l.x, l.y);
+            add_x2(y[2], y[3], l.z, l.w);
+          } else {
+            add_x2(y[0], y[1], nd, nd);
+            add_x2(y[2], y[3], nd, nd);
+          }
+          mul_x2(x[c], x[c + 1], y[0], y[1]);
+          mul_x2(x[c + 2], x[c + 3], y[2], y[3]);
+        }
+      }
+      {
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
+        tmem_st32(tDP, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl->ds_full);
+          if (kKeys) mbar_arrive(&ctl->stat_empty[n & 1u]);
+        }
+      }
+      if constexpr (kGrad) {
+        if (!stored) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) x[c] = 0.f;
+        }
+        if (near) {
+          // Sums by diagonal of this warp's 32 rows x 64 columns: the running
+          // sum of a diagonal moves to the next lane with each column, and
+          // leaves at lane 31 (entry c) or after the last column.
+          const uint32_t buf = n_near & 1u;
+          if (n_near >= 2 && !wait_warp(&ctl->sum_empty[buf], ((n_near >> 1) - 1) & 1u, w,
+                                        kBSiteSumEmpty)) {
+            ok = false;
+            break;
+          }
+          float* out = sSum + (buf * 8 + warp) * 96;
+          float s = 0.f;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const float up = __shfl_up_sync(0xffffffffu, s, 1);
+            s = (lane == 0 ? 0.f : up) + x[c];
+            if (lane == 31) out[c] = s;
+          }
+          if (lane < 31) out[94 - lane] = s;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->sum_full[buf]);
+          ++n_near;
+        } else {
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            add_x2(acc[0], acc[1], x[c], x[c + 1]);
+            add_x2(acc[2], acc[3], x[c + 2], x[c + 3]);
+          }
+          const float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          if (rel0 < 0) far_lo += s;
+          else far_hi += s;
+        }
+      }
+    }
+    if constexpr (kGrad) {
+      if (!ok) break;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        far_lo += __shfl_xor_sync(0xffffffffu, far_lo, d);
+        far_hi += __shfl_xor_sync(0xffffffffu, far_hi, d);
+      }
+      if (n_far > 0 && !wait_warp(&ctl->far_empty, (n_far - 1) & 1u, w, kBSiteFarEmpty)) break;
+      ++n_far;
+      if (lane == 0) {
+        ctl->far[warp][0] = far_lo;
+        ctl->far[warp][1] = far_hi;
+        mbar_arrive(&ctl->far_full);
+      }
+    }
+  }
+}
+
+// Bias gradient (one warp, query walk): the item's sums by distance, entry e
+// for the distance e - reach - kRelPad, each written once. Diagonal d of a
+// tile (d = column - row + 127) gathers entry x = d - 96 - 64 g + 32 wq of
+// each math warp (g, wq); the diagonals 128..254 of a tile are 0..126 of the
+// next one and wait for it in registers. Entry 0 and the last take the tiles
+// past the reach, which near tiles cannot touch.
+template <int D>
+__device__ void bwd_sums(const BwdParams& p, BCtl* ctl, const float* sSum, const WaitCtx& w) {
+  const int lane = threadIdx.x & 31;
+  const int width = rel_width(p.rel.reach);
+  uint32_t n_near = 0, n_far = 0;
+  for (int k = 0;; ++k) {
+    const int idx = bwd_item(k);
+    if (idx >= p.n_q) return;
+    const BwdItem it = p.q_items[idx];
+    float* out = p.rel_part + (int64_t)it.stat * width;
+    for (int e = lane; e < width; e += 32) out[e] = 0.f;
+    __syncwarp();
+    if (it.hi <= it.lo) continue;
+    const SeqRec sr = p.seqs[it.b];
+    const int diag0 = -(it.tile * 128 + 127 + (sr.skv - sr.sq)) + p.rel.reach + kRelPad;
+    float carry[4] = {0.f, 0.f, 0.f, 0.f};
+    int pending = -1;  // entry of carry[0] of lane 0
+    for (int t = it.lo; t < it.hi; ++t) {
+      const int top = t * 128 + 127 - (it.tile * 128 + (sr.skv - sr.sq));
+      if (top <= -p.rel.reach || top - 254 >= p.rel.reach) continue;
+      const uint32_t buf = n_near & 1u;
+      if (!wait_warp(&ctl->sum_full[buf], (n_near >> 1) & 1u, w, kBSiteSumFull)) return;
+      const float* in = sSum + buf * 8 * 96;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int d = q * 32 + lane;
+        float lo = carry[q], hi = 0.f;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          const int x = d - (96 + 64 * (m >> 2) - 32 * (m & 3));
+          if (x >= 0 && x < 95) lo += in[m * 96 + x];
+          if (x + 128 >= 0 && x + 128 < 95) hi += in[m * 96 + x + 128];
+        }
+        out[diag0 + t * 128 + d] = lo;
+        carry[q] = hi;
+      }
+      pending = diag0 + (t + 1) * 128;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->sum_empty[buf]);
+      ++n_near;
+    }
+    if (pending >= 0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) out[pending + q * 32 + lane] = carry[q];
+    }
+    if (!wait_warp(&ctl->far_full, n_far & 1u, w, kBSiteFarFull)) return;
+    ++n_far;
+    __syncwarp();
+    if (lane < 2) {
+      float s = 0.f;
+#pragma unroll
+      for (int m = 0; m < 8; ++m) s += ctl->far[m][lane];
+      out[lane ? width - 1 : 0] = s;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->far_empty);
+  }
+}
+
+// Epilogue (one warpgroup, one row per thread): accumulators, times a factor,
+// to bf16 rows in global memory (zeros for items without a tile). In the
+// query walk it also brings Q and dO of the next item into tensor memory, a
+// row per thread, once the last product of the current item that reads them
+// is done.
+template <int D, bool kKeys>
+__device__ void bwd_epilogue(const BwdParams& p, BCtl* ctl, uint32_t tmem, const WaitCtx& w) {
+  using C = BCfg<D, kKeys>;
+  const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int row = wq * 32 + lane;
+  const uint32_t lane_bits = (uint32_t)(wq * 32) << 16;
+  const BwdItem* items = kKeys ? p.k_items : p.q_items;
+  const int n_items = kKeys ? p.n_k : p.n_q;
+  const int64_t sb = kKeys ? p.k_sb : p.q_sb, sh = kKeys ? p.k_sh : p.q_sh,
+                st = kKeys ? p.k_st : p.q_st;
+  uint32_t held = 0;  // items with tiles whose Q and dO are in tensor memory
+  uint32_t done = 0;  // items with tiles written out
+  auto fetch = [&](const BwdItem& it) -> bool {
+    const SeqRec sr = p.seqs[it.b];
+    const int i = it.tile * 128 + row;
+    const bool stored = i < sr.sq;
+    const int64_t off = it.b * sb + it.h * sh + ((int64_t)sr.q_off + (stored ? i : 0)) * st;
+#pragma unroll 1
+    for (int a = 0; a < 2; ++a) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          reinterpret_cast<const __nv_bfloat16*>(a ? p.d_o : p.q) + off);
+      uint32_t v[D / 2];
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) {
+        const uint4 u = stored ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
+        v[4 * x] = u.x;
+        v[4 * x + 1] = u.y;
+        v[4 * x + 2] = u.z;
+        v[4 * x + 3] = u.w;
+      }
+      if (held > 0 && !wait_warp(a ? &ctl->a1_empty : &ctl->a0_empty, (held - 1) & 1u, w,
+                                 a ? kBSiteA1Empty : kBSiteA0Empty))
+        return false;
+      tc_fence_after();
+      const uint32_t dst = tmem + lane_bits + (a ? C::kColA1 : C::kColA0);
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x)
+        tmem_st32(dst + 32u * x, *reinterpret_cast<const uint32_t(*)[32]>(&v[32 * x]));
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a ? &ctl->a1_full : &ctl->a0_full);
+    }
+    ++held;
+    return true;
+  };
+  auto store_acc = [&](const BwdItem& it, const SeqRec& sr, int which, void* dst, float mul) -> bool {
+    const int at = it.tile * 128 + row;
+    const bool stored = at < (kKeys ? sr.skv : sr.sq);
+    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(dst) + it.b * sb + it.h * sh +
+                       ((int64_t)(kKeys ? sr.kv_off : sr.q_off) + at) * st;
+    const bool v8 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
+    if (it.hi <= it.lo) {
+      if (stored)
+#pragma unroll 1
+        for (int x = 0; x < D / 8; ++x)
+          st_global_na_v4(reinterpret_cast<uint4*>(o) + x, make_uint4(0u, 0u, 0u, 0u));
+      return true;
+    }
+    if (!wait_warp(&ctl->acc_full[which], done & 1u, w, kBSiteAccFull)) return false;
+    tc_fence_after();
+    const uint32_t src = tmem + lane_bits + (which ? C::kColAcc1 : C::kColAcc0);
+#pragma unroll 1
+    for (int ch = 0; ch < D / 32; ++ch) {
+      uint32_t ov[32];
+      tmem_ld32_wait(src + ch * 32u, ov);
+      uint4 pk[4];
+      uint32_t* pw = reinterpret_cast<uint32_t*>(pk);
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        pw[c] = pack_bf16(__uint_as_float(ov[2 * c]) * mul, __uint_as_float(ov[2 * c + 1]) * mul);
+      if (stored) {
+        uint4* q = reinterpret_cast<uint4*>(o + ch * 32);
+        if (v8) {
+          st_global_na_v8(q, pk[0], pk[1]);
+          st_global_na_v8(q + 2, pk[2], pk[3]);
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) st_global_na_v4(q + v, pk[v]);
+        }
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->acc_free[which]);
+    return true;
+  };
+  int ahead = 0;  // list position from which the next item with tiles is looked for
+  auto fetch_next = [&]() -> bool {
+    if constexpr (!kKeys) {
+      for (int idx; (idx = bwd_item(ahead)) < n_items;) {
+        ++ahead;
+        const BwdItem it = items[idx];
+        if (it.hi > it.lo) return fetch(it);
+      }
+    }
+    return true;
+  };
+  if (!fetch_next()) return;
+  for (int k = 0;; ++k) {
+    const int idx = bwd_item(k);
+    if (idx >= n_items) break;
+    const BwdItem it = items[idx];
+    const SeqRec sr = p.seqs[it.b];
+    const bool live = it.hi > it.lo;
+    if (live && !fetch_next()) return;
+    if constexpr (kKeys) {
+      if (!store_acc(it, sr, 1, p.dv, 1.f)) return;
+      if (!store_acc(it, sr, 0, p.dk, p.scale)) return;
+    } else {
+      if (!store_acc(it, sr, 0, p.dq, p.scale)) return;
+    }
+    if (live) ++done;
+  }
+}
+
+template <int D, bool kKeys, int kBias>
+__global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_constant__ BwdParams p) {
+  using C = BCfg<D, kKeys>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sA = smem;
+  uint8_t* sB0 = sA + C::kABytes;
+  uint8_t* sB1 = sB0 + C::kN0 * C::kTileBytes;
+  uint8_t* sStat = sB1 + C::kN1 * C::kTileBytes;
+  float* sSum = reinterpret_cast<float*>(sStat + C::kStatBytes);
+  auto* ctl = reinterpret_cast<BCtl*>(sStat + C::kStatBytes + C::kSumBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The two walks need nothing of each other: the next launch of the stream
+  // may take each SM this one leaves.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(p.err_word, kErrTimeout | (kBSiteSmem << kErrWhereShift));
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&ctl->b0_full[s], 1);
+      mbar_init(&ctl->b0_empty[s], 1);
+      mbar_init(&ctl->b1_full[s], 1);
+      mbar_init(&ctl->b1_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->stat_full[s], 1);
+      mbar_init(&ctl->stat_empty[s], 8);
+      mbar_init(&ctl->acc_full[s], 1);
+      mbar_init(&ctl->acc_free[s], 4);
+      mbar_init(&ctl->sum_full[s], 8);
+      mbar_init(&ctl->sum_empty[s], 1);
+    }
+    mbar_init(&ctl->fix, 1);
+    mbar_init(&ctl->a0_full, kKeys ? 1 : 4);
+    mbar_init(&ctl->a1_full, kKeys ? 1 : 4);
+    mbar_init(&ctl->a0_empty, 1);
+    mbar_init(&ctl->a1_empty, 1);
+    mbar_init(&ctl->s_full, 1);
+    mbar_init(&ctl->s_free, 8);
+    mbar_init(&ctl->p_full, 8);
+    mbar_init(&ctl->dp_full, 1);
+    mbar_init(&ctl->ds_full, 8);
+    mbar_init(&ctl->far_full, 8);
+    mbar_init(&ctl->far_empty, 1);
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) {
+    asm volatile(
+        "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+            smem_u32(&ctl->tmem_base)),
+        "r"(C::kTmemCols)
+        : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const WaitCtx w{&ctl->abort_flag, p.err_word, p.timeout_ns};
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwdRegsMath));
+    bwd_math<D, kKeys, kBias>(p, ctl, tmem, sStat, sSum, w);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwdRegsEpi));
+    bwd_epilogue<D, kKeys>(p, ctl, tmem, w);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwdRegsControl));
+    if (warp == 12 && lane == 0) bwd_mma<D, kKeys>(p, ctl, tmem, sA, sB0, sB1, w);
+    if (warp == 13) bwd_load<D, kKeys>(p, ctl, sA, sB0, sB1, sStat, w);
+    if constexpr (kBias == kBwdBiasRel && !kKeys)
+      if (warp == 15) bwd_sums<D>(p, ctl, sSum, w);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(C::kTmemCols)
+                 : "memory");
+  }
+  // The key walk may have started beside the query walk: it ends after it,
+  // so that what follows in the stream follows both.
+  if constexpr (kKeys) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+}  // namespace dev
+
+// ----------------------------------------------------------------- host
+
+template <int D, bool kKeys, int kBias>
+static cudaError_t launch_walk(const BwdParams& p, int grid, bool beside, cudaStream_t stream,
+                               const char** why) {
+  using C = dev::BCfg<D, kKeys>;
+  auto kern = dev::fa_bwd_sm100<D, kKeys, kBias>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  static int regs = 0;  // the same on every device: one architecture
+  if (regs == 0) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    regs = attr.numRegs;
+  }
+  // setmaxnreg redistributes the registers the CTA was launched with; a split
+  // larger than that allocation would never be granted.
+  if (regs < 128) {
+    if (why) *why = "kernel compiled with fewer registers than its warpgroup split needs";
+    return cudaErrorInvalidConfiguration;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(dev::kBwdThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int D, int kBias>
+static cudaError_t launch_both(const BwdParams& p, int num_sms, cudaStream_t stream,
+                               const char** why) {
+  if (p.n_q > 0) {
+    const cudaError_t e = launch_walk<D, false, kBias>(p, p.n_q < num_sms ? p.n_q : num_sms, false,
+                                                       stream, why);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.n_k <= 0) return cudaSuccess;
+  return launch_walk<D, true, kBias>(p, p.n_k < num_sms ? p.n_k : num_sms, p.n_q > 0, stream, why);
+}
+
+cudaError_t launch_bwd(int D, const BwdParams& p, int num_sms, cudaStream_t stream,
+                       const char** why) {
+  auto pick = [&](auto dim) {
+    constexpr int kD = decltype(dim)::value;
+    if (p.rel.ext) return launch_both<kD, dev::kBwdBiasRel>(p, num_sms, stream, why);
+    if (p.slopes) return launch_both<kD, dev::kBwdBiasAlibi>(p, num_sms, stream, why);
+    return launch_both<kD, dev::kBwdBiasNone>(p, num_sms, stream, why);
+  };
+  return D == 128 ? pick(std::integral_constant<int, 128>{}) : pick(std::integral_constant<int, 64>{});
+}
+
+}  // namespace fa
