@@ -23,7 +23,7 @@
 //   warps 0-7   P and dS; warps 0-3 columns 0..63 of a tile, 4-7 64..127
 //   warps 8-11  epilogue: accumulators to global memory; query walk: Q and
 //               dO of the next item from global to tensor memory
-//   warp 12     all MMAs (one thread; owns tensor memory)
+//   warp 12     all MMAs (one lane issues; owns tensor memory)
 //   warp 13     TMA loads; clears the rows of a streamed tile that belong to
 //               the next packed sequence
 //   warp 14     idle
@@ -55,6 +55,8 @@ static_assert(256 * kBwdRegsMath + 128 * kBwdRegsEpi + 128 * kBwdRegsControl == 
               "register split must equal the launch allocation");
 constexpr int kBwdBiasNone = 0, kBwdBiasAlibi = 1, kBwdBiasRel = 2;
 constexpr float kLog2e = 1.4426950408889634f;
+// Of 8 pairs of columns, how many take the FMA-pipe exponential.
+constexpr int kPolyOf8 = 3;
 
 // Where a wait gave up (error word bits 8..15), after the forward's sites.
 enum BwdSite : uint32_t {
@@ -93,7 +95,7 @@ struct BCtl {
   uint64_t fix;                          // a tile whose tail the load warp clears
   uint64_t a0_full, a0_empty, a1_full, a1_empty;
   uint64_t s_full, s_free;   // S in tensor memory / read into registers (query walk)
-  uint64_t p_full;           // P in tensor memory (key walk)
+  uint64_t p_full[2];        // half of P's columns in tensor memory (key walk)
   uint64_t dp_full, ds_full;
   uint64_t acc_full[2], acc_free[2];
   uint64_t sum_full[2], sum_empty[2];    // bias gradient: sums by diagonal of one tile
@@ -114,6 +116,40 @@ __device__ __forceinline__ void mul_x2(float& a, float& b, float x, float y) {
       "mov.b64 {%0, %1}, r;\n\t}"
       : "+f"(a), "+f"(b)
       : "f"(x), "f"(y));
+}
+
+// 2^x for two values on the FMA pipe: x = n + f with n = floor(x) (adding
+// 1.5 * 2^23 rounded down leaves n in the low mantissa bits), a polynomial of
+// degree kDeg for 2^f on [0, 1) and n added into the exponent field. p(0) = 1
+// exactly, so that x <= -127 (a masked pair) gives 0. Relative error 3.0e-6
+// (degree 4) and 1.6e-7 (degree 5); coefficients from gen_exp2_poly.py.
+template <int kDeg>
+__device__ __forceinline__ void ex2_floor_x2(float& a, float& b) {
+  static_assert(kDeg == 4 || kDeg == 5, "fitted degrees");
+  constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
+  constexpr float kC[2][6] = {
+      {1.0f, 0.69304484f, 0.2412802f, 0.052242473f, 0.013426684f, 0.0f},
+      {1.0f, 0.6931513f, 0.24016444f, 0.055799913f, 0.009017031f, 0.00186713f}};
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(a));  // -127
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(b));
+  float ta = a, tb = b;
+  asm("{\n\t.reg .b64 r, s;\n\t"
+      "mov.b64 r, {%0, %1};\n\t"
+      "mov.b64 s, {%2, %2};\n\t"
+      "add.rm.f32x2 r, r, s;\n\t"
+      "mov.b64 {%0, %1}, r;\n\t}"
+      : "+f"(ta), "+f"(tb)
+      : "f"(kShift));
+  float fa = ta, fb = tb;
+  add_x2(fa, fb, -kShift, -kShift);                              // n
+  fma_x2(fa, fb, pack_f32x2(-1.f, -1.f), pack_f32x2(a, b));      // f = x - n
+  const uint64_t f2 = pack_f32x2(fa, fb);
+  float pa = kC[kDeg - 4][kDeg], pb = pa;
+#pragma unroll
+  for (int i = kDeg - 1; i >= 0; --i)
+    fma_x2(pa, pb, f2, pack_f32x2(kC[kDeg - 4][i], kC[kDeg - 4][i]));
+  a = __int_as_float(__float_as_int(pa) + (__float_as_int(ta) << 23));
+  b = __int_as_float(__float_as_int(pb) + (__float_as_int(tb) << 23));
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
@@ -268,16 +304,24 @@ __device__ void bwd_load(const BwdParams& p, BCtl* ctl, uint8_t* sA, uint8_t* sB
   __syncwarp();
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // D[128 x 128] = A B^T, both K-major over the head dim; A in shared memory
 // (key walk) or tensor memory.
 template <int D, bool kKeys>
-__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a_tmem, const uint8_t* a_smem,
-                                             const uint8_t* b_smem) {
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a_tmem, uint64_t a0, uint64_t b0) {
   using C = BCfg<D, kKeys>;
   constexpr uint32_t idesc = idesc_bf16(128, 128, false);
-  const uint64_t b0 = sdesc(smem_u32(b_smem), 16u, 1024u);
-  const uint64_t a0 = sdesc(smem_u32(a_smem), 16u, 1024u);
-#pragma unroll 1
+#pragma unroll
   for (int k = 0; k < D / 16; ++k) {
     const uint64_t off = (uint64_t)(((k >> 2) * C::kChunkBytes + (k & 3) * 32u) >> 4);
     if constexpr (kKeys) mma_ss(d, a0 + off, b0 + off, idesc, k > 0 ? 1u : 0u);
@@ -285,23 +329,26 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a_tmem, const 
   }
 }
 
-// acc[128 x D] += W B with W (P or dS, bf16) in tensor memory: columns
-// 0..63 in the first 32 tensor memory columns from `a`, 64..127 from a + 64.
+// acc[128 x D] += W B over half of W's columns, W (P or dS, bf16) in tensor
+// memory: columns 0..63 in the first 32 tensor memory columns from `a`,
+// 64..127 from a + 64. Half 0 takes the columns 0..31 and 64..95 (what each
+// math warp stores first), half 1 the others.
 template <int D, bool kKeys>
-__device__ __forceinline__ void issue_acc(uint32_t d, uint32_t a, const uint8_t* b_smem,
-                                          bool accumulate) {
-  using C = BCfg<D, kKeys>;
+__device__ __forceinline__ void issue_acc(uint32_t d, uint32_t a, uint64_t b0, uint32_t accumulate,
+                                          int half) {
   constexpr uint32_t idesc = idesc_bf16(128, D, true);
-  const uint64_t b0 = sdesc(smem_u32(b_smem), C::kChunkBytes, 1024u);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
+  for (int q = 0; q < 4; ++q) {
+    const int k = (q >> 1) * 4 + half * 2 + (q & 1);  // 16 columns of W, 16 rows of B
     mma_ts(d, a + (k >> 2) * 64u + (k & 3) * 8u, b0 + (uint64_t)(k * (2048u >> 4)), idesc,
-           (accumulate || k > 0) ? 1u : 0u);
+           q > 0 ? 1u : accumulate);
+  }
 }
 
-// All products (one thread). The products that overwrite tensor memory which
-// an earlier product still reads are issued after it by this same thread:
-// products execute in order.
+// All products (a whole warp, so that addresses and descriptors stay in
+// uniform registers; one lane issues). The products that overwrite tensor
+// memory which an earlier product still reads are issued after it by this
+// same thread: products execute in order.
 template <int D, bool kKeys>
 __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint8_t* sA,
                         const uint8_t* sB0, const uint8_t* sB1, const WaitCtx& w) {
@@ -309,6 +356,14 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
   const BwdItem* items = kKeys ? p.k_items : p.q_items;
   const int n_items = kKeys ? p.n_k : p.n_q;
   const uint32_t tS = tmem + C::kColS, tDP = tmem + C::kColDP;
+  // Descriptors of slot 0: K-major (scores) and MN-major (accumulation).
+  const uint64_t dA0 = sdesc(smem_u32(sA), 16u, 1024u);
+  const uint64_t dA1 = sdesc(smem_u32(sA) + C::kTileBytes, 16u, 1024u);
+  const uint64_t dB0 = sdesc(smem_u32(sB0), 16u, 1024u);
+  const uint64_t dB1 = sdesc(smem_u32(sB1), 16u, 1024u);
+  const uint64_t dM0 = sdesc(smem_u32(sB0), C::kChunkBytes, 1024u);
+  const uint64_t dM1 = sdesc(smem_u32(sB1), C::kChunkBytes, 1024u);
+  constexpr uint64_t kSlot = C::kTileBytes >> 4;
   Step cur, nx;
   nx.k = 0;
   nx.valid = false;
@@ -316,63 +371,98 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
   uint32_t n = 0;       // step of nx
   uint32_t a0 = 0, a1 = 0;  // held operands awaited
   uint32_t items_done = 0;
-  auto scores = [&]() -> bool {
-    if (nx.first && !wait_bounded(&ctl->a0_full, a0++ & 1u, w, kBSiteA0Full)) return false;
-    const uint32_t st = n % C::kN0;
-    if (!wait_bounded(&ctl->b0_full[st], (n / C::kN0) & 1u, w, kBSiteB0Full)) return false;
-    if (!kKeys && n > 0 && !wait_bounded(&ctl->s_free, (n - 1) & 1u, w, kBSiteSFree)) return false;
-    tc_fence_after();
-    issue_scores<D, kKeys>(tS, tmem + C::kColA0, sA, sB0 + st * C::kTileBytes);
-    mma_commit(&ctl->s_full);
-    if (nx.last) mma_commit(&ctl->a0_empty);
-    return true;
+  // The operands of the products of step nx are waited for ahead of the
+  // products that they follow, so that those waits (about 100 cycles each
+  // even when the data is there) do not fall between two products.
+  auto operands0 = [&]() -> bool {
+    if (nx.first && !wait_warp(&ctl->a0_full, a0++ & 1u, w, kBSiteA0Full)) return false;
+    return wait_warp(&ctl->b0_full[n % C::kN0], (n / C::kN0) & 1u, w, kBSiteB0Full);
   };
-  auto dprobs = [&]() -> bool {
-    if (nx.first && !wait_bounded(&ctl->a1_full, a1++ & 1u, w, kBSiteA1Full)) return false;
-    const uint32_t st = n % C::kN1;
-    if (!wait_bounded(&ctl->b1_full[st], (n / C::kN1) & 1u, w, kBSiteB1Full)) return false;
-    tc_fence_after();
-    issue_scores<D, kKeys>(tDP, tmem + C::kColA1, sA + C::kTileBytes, sB1 + st * C::kTileBytes);
-    mma_commit(&ctl->dp_full);
-    if (!kKeys) mma_commit(&ctl->b1_empty[st]);
-    if (nx.last) mma_commit(&ctl->a1_empty);
-    return true;
+  auto operands1 = [&]() -> bool {
+    if (nx.first && !wait_warp(&ctl->a1_full, a1++ & 1u, w, kBSiteA1Full)) return false;
+    return wait_warp(&ctl->b1_full[n % C::kN1], (n / C::kN1) & 1u, w, kBSiteB1Full);
   };
-  bool ok = !nx.valid || (scores() && dprobs());
+  auto scores = [&]() {
+    if (elect_one()) {
+      issue_scores<D, kKeys>(tS, tmem + C::kColA0, dA0, dB0 + (n % C::kN0) * kSlot);
+      mma_commit(&ctl->s_full);
+      if (nx.last) mma_commit(&ctl->a0_empty);
+    }
+    __syncwarp();
+  };
+  auto dprobs = [&]() {
+    if (elect_one()) {
+      issue_scores<D, kKeys>(tDP, tmem + C::kColA1, dA1, dB1 + (n % C::kN1) * kSlot);
+      mma_commit(&ctl->dp_full);
+      if (!kKeys) mma_commit(&ctl->b1_empty[n % C::kN1]);
+      if (nx.last) mma_commit(&ctl->a1_empty);
+    }
+    __syncwarp();
+  };
+  bool ok = !nx.valid || (operands0() && operands1());
+  if (ok && nx.valid) {
+    tc_fence_after();
+    scores();
+    dprobs();
+  }
   while (ok && nx.valid) {
     cur = nx;
     const uint32_t c = n;
     next_step(items, n_items, nx);
     ++n;
+    if (nx.valid && !operands0()) break;
     if constexpr (kKeys) {
-      if (!wait_bounded(&ctl->p_full, c & 1u, w, kBSitePFull)) break;
+      // dV in two halves of the queries: the first while the other half's P
+      // is computed.
       if (cur.first && items_done > 0 &&
-          !wait_bounded(&ctl->acc_free[1], (items_done - 1) & 1u, w, kBSiteAccFree))
+          !wait_warp(&ctl->acc_free[1], (items_done - 1) & 1u, w, kBSiteAccFree))
         break;
-      tc_fence_after();
       const uint32_t st = c % C::kN1;
-      issue_acc<D, kKeys>(tmem + C::kColAcc1, tS, sB1 + st * C::kTileBytes, !cur.first);
-      mma_commit(&ctl->b1_empty[st]);
-      if (cur.last) mma_commit(&ctl->acc_full[1]);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!wait_warp(&ctl->p_full[half], c & 1u, w, kBSitePFull)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          issue_acc<D, kKeys>(tmem + C::kColAcc1, tS, dM1 + st * kSlot,
+                              (cur.first && half == 0) ? 0u : 1u, half);
+          if (half) {
+            mma_commit(&ctl->b1_empty[st]);
+            if (cur.last) mma_commit(&ctl->acc_full[1]);
+          }
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (nx.valid) scores();
+    } else if (nx.valid) {
+      if (!wait_warp(&ctl->s_free, c & 1u, w, kBSiteSFree)) break;
+      tc_fence_after();
+      scores();
     }
-    if (nx.valid && !scores()) break;
-    if (!wait_bounded(&ctl->ds_full, c & 1u, w, kBSiteDsFull)) break;
+    if (nx.valid && !operands1()) break;
     if (cur.first && items_done > 0 &&
-        !wait_bounded(&ctl->acc_free[0], (items_done - 1) & 1u, w, kBSiteAccFree))
+        !wait_warp(&ctl->acc_free[0], (items_done - 1) & 1u, w, kBSiteAccFree))
       break;
+    if (!wait_warp(&ctl->ds_full, c & 1u, w, kBSiteDsFull)) break;
     tc_fence_after();
     const uint32_t st = c % C::kN0;
-    issue_acc<D, kKeys>(tmem + C::kColAcc0, tDP, sB0 + st * C::kTileBytes, !cur.first);
-    mma_commit(&ctl->b0_empty[st]);
-    if (cur.last) {
-      mma_commit(&ctl->acc_full[0]);
-      ++items_done;
+    if (elect_one()) {
+      issue_acc<D, kKeys>(tmem + C::kColAcc0, tDP, dM0 + st * kSlot, cur.first ? 0u : 1u, 0);
+      issue_acc<D, kKeys>(tmem + C::kColAcc0, tDP, dM0 + st * kSlot, 1u, 1);
+      mma_commit(&ctl->b0_empty[st]);
+      if (cur.last) mma_commit(&ctl->acc_full[0]);
     }
-    if (nx.valid && !dprobs()) break;
+    __syncwarp();
+    if (cur.last) ++items_done;
+    if (nx.valid) dprobs();
   }
-  // Wait until every MMA this thread issued (and its commits) has finished
-  // with tensor and shared memory.
-  mma_commit(&ctl->drain);
+  // Wait until every product issued here (and its commits) has finished with
+  // tensor and shared memory.
+  if (elect_one()) mma_commit(&ctl->drain);
+  __syncwarp();
   wait_bounded(&ctl->drain, 0u, w, kBSiteDrain, false);
 }
 
@@ -565,16 +655,27 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
           x[c] = ((wm[c >> 5] >> (c & 31)) & 1u) ? x[c] : -INFINITY;
       }
 #pragma unroll
-      for (int c = 0; c < 64; ++c) x[c] = ex2(x[c]);
-      if constexpr (kKeys) {
-        uint32_t pk[32];
+      for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
-        tmem_st32(tS, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full);
+        for (int c = 32 * half; c < 32 * half + 32; c += 2) {
+          if (((c >> 1) * kPolyOf8) % 8 < kPolyOf8) {
+            ex2_floor_x2<kGrad ? 5 : 4>(x[c], x[c + 1]);
+          } else {
+            x[c] = ex2(x[c]);
+            x[c + 1] = ex2(x[c + 1]);
+          }
+        }
+        if constexpr (kKeys) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            pk[c] = pack_bf16(x[32 * half + 2 * c], x[32 * half + 2 * c + 1]);
+          tmem_st16(tS + 16u * half, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->p_full[half]);
+        }
       }
       if (!wait_warp(&ctl->dp_full, n & 1u, w, kBSiteDpFull)) {
         ok = false;
@@ -868,7 +969,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
   uint8_t* sStat = sB1 + C::kN1 * C::kTileBytes;
   float* sSum = reinterpret_cast<float*>(sStat + C::kStatBytes);
   auto* ctl = reinterpret_cast<BCtl*>(sStat + C::kStatBytes + C::kSumBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   // The two walks need nothing of each other: the next launch of the stream
   // may take each SM this one leaves.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -886,6 +987,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->stat_full[s], 1);
       mbar_init(&ctl->stat_empty[s], 8);
+      mbar_init(&ctl->p_full[s], 8);
       mbar_init(&ctl->acc_full[s], 1);
       mbar_init(&ctl->acc_free[s], 4);
       mbar_init(&ctl->sum_full[s], 8);
@@ -898,7 +1000,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
     mbar_init(&ctl->a1_empty, 1);
     mbar_init(&ctl->s_full, 1);
     mbar_init(&ctl->s_free, 8);
-    mbar_init(&ctl->p_full, 8);
     mbar_init(&ctl->dp_full, 1);
     mbar_init(&ctl->ds_full, 8);
     mbar_init(&ctl->far_full, 8);
@@ -918,7 +1019,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
   const WaitCtx w{&ctl->abort_flag, p.err_word, p.timeout_ns};
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwdRegsMath));
@@ -928,7 +1029,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
     bwd_epilogue<D, kKeys>(p, ctl, tmem, w);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwdRegsControl));
-    if (warp == 12 && lane == 0) bwd_mma<D, kKeys>(p, ctl, tmem, sA, sB0, sB1, w);
+    if (warp == 12) bwd_mma<D, kKeys>(p, ctl, tmem, sA, sB0, sB1, w);
     if (warp == 13) bwd_load<D, kKeys>(p, ctl, sA, sB0, sB1, sStat, w);
     if constexpr (kBias == kBwdBiasRel && !kKeys)
       if (warp == 15) bwd_sums<D>(p, ctl, sSum, w);

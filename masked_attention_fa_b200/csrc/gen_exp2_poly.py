@@ -49,9 +49,32 @@ def remez_relative(degree, a=-0.5, b=0.5, iters=30):
     return c, float(np.abs(err).max())
 
 
+def remez_from_one(degree, iters=50):
+    """The same for 2^f on [0, 1) with c0 = 1 exactly (n = floor(x), the backward pass)."""
+    n = degree
+    grid = np.linspace(0.0, 1.0, 400001)[1:]
+    ref = np.clip(0.5 - 0.5 * np.cos(np.pi * (np.arange(n + 1) + 0.7) / (n + 0.7)), 1e-3, 1.0)
+    for _ in range(iters):
+        A = np.zeros((n + 1, n + 1))
+        for i, x in enumerate(ref):
+            A[i, :n] = x ** np.arange(1, n + 1)
+            A[i, n] = -((-1) ** i) * np.exp2(x)
+        c = np.concatenate([[1.0], np.linalg.solve(A, np.exp2(ref) - 1.0)[:n]])
+        err = np.polyval(c[::-1], grid) / np.exp2(grid) - 1.0
+        runs = np.split(np.arange(len(grid)), np.flatnonzero(np.diff(np.sign(err))) + 1)
+        peaks = [r[np.abs(err[r]).argmax()] for r in runs]
+        if len(peaks) >= n + 1:
+            ref = grid[peaks[-(n + 1):]]
+    return c, float(np.abs(err).max())
+
+
 if __name__ == "__main__":
     deg = int(sys.argv[1]) if len(sys.argv) > 1 else 3
     c, e = remez_relative(deg)
     for i, ci in enumerate(c):
         print(f"c{i} = {np.float32(ci)!r}  # {ci:.17g}")
     print(f"max relative error on [-1/2, 1/2]: {e:.3e}")
+    c, e = remez_from_one(deg)
+    for i, ci in enumerate(c):
+        print(f"c{i} = {np.float32(ci)!r}  # {ci:.17g}")
+    print(f"c0 = 1, max relative error on [0, 1): {e:.3e}")
