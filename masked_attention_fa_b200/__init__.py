@@ -10,7 +10,6 @@ The C entry points keep their names (``fa_create``, ``fa_fwd``, ...). The
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -69,7 +68,7 @@ class fa_split_part_t(ctypes.Structure):
 class fa_relbias_t(ctypes.Structure):
     _fields_ = [
         ("table", ctypes.c_void_p),
-        ("bucket_of", ctypes.POINTER(ctypes.c_int32)),
+        ("bucket_of", ctypes.c_void_p),
         ("num_buckets", ctypes.c_int32),
         ("reach", ctypes.c_int32),
     ]
@@ -88,7 +87,7 @@ def load_library():
                           "`python -m masked_attention_fa_b200.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.c_void_p
-    i64p = ctypes.POINTER(ctypes.c_int64)
+    i64p = P  # host int64 arrays, passed as addresses
     dp = ctypes.POINTER(fa_desc_t)
     st = ctypes.c_int32
     lib.fa_create.argtypes = [dp, ctypes.POINTER(P)]
@@ -183,9 +182,7 @@ class _Arrays:
 
     @staticmethod
     def _p(a):
-        if a is None:
-            return None
-        return a.ctypes.data_as(ctypes.POINTER(ctypes.c_int64))
+        return None if a is None else a.__array_interface__["data"][0]
 
     def ptrs(self):
         return self._p(self.prefix), self._p(self.cu_q), self._p(self.cu_kv)
@@ -266,7 +263,7 @@ def fa_sync_status(h) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def fa_fwd(h, q, k, v, o, lse, atten_mask=None, prefix=None, actual_seq_qlen=None,
@@ -289,7 +286,7 @@ def fa_fwd_alibi(h, q, k, v, slopes, o, lse, prefix=None, actual_seq_qlen=None,
     a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
     _check(load_library().fa_fwd_alibi(h, _ptr(q), _ptr(k), _ptr(v), _ptr(slopes), *a.ptrs(),
                                        _ptr(o), _ptr(lse),
-                                       ctypes.c_void_p(_stream_int(stream, q.device))))
+                                       _stream_int(stream, q.device)))
 
 
 def _relbias(table, bucket_of):
@@ -298,8 +295,8 @@ def _relbias(table, bucket_of):
     m = np.ascontiguousarray(bucket_of, dtype=np.int32)
     if m.ndim != 1 or m.size < 3 or m.size % 2 == 0:
         raise ValueError("the bucket map must have 2 * reach + 1 entries, reach >= 1")
-    b = fa_relbias_t(table.data_ptr(), m.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)),
-                     int(table.shape[0]), m.size // 2)
+    b = fa_relbias_t(table.data_ptr(), m.__array_interface__["data"][0], table.shape[0],
+                     m.size // 2)
     return b, m
 
 
@@ -333,7 +330,7 @@ def fa_fwd_relbias(h, q, k, v, table, bucket_of, o, lse, prefix=None, actual_seq
     b, keep = _relbias(table, bucket_of)
     _check(load_library().fa_fwd_relbias(h, _ptr(q), _ptr(k), _ptr(v), ctypes.byref(b), *a.ptrs(),
                                          _ptr(o), _ptr(lse),
-                                         ctypes.c_void_p(_stream_int(stream, q.device))))
+                                         _stream_int(stream, q.device)))
 
 
 def fa_bwd(h, q, k, v, o, lse, d_o, dq, dk, dv, atten_mask=None, d_lse=None, prefix=None,
@@ -342,7 +339,7 @@ def fa_bwd(h, q, k, v, o, lse, d_o, dq, dk, dv, atten_mask=None, d_lse=None, pre
     a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
     _check(load_library().fa_bwd(h, _ptr(q), _ptr(k), _ptr(v), _ptr(atten_mask), _ptr(o),
                                  _ptr(lse), _ptr(d_o), _ptr(d_lse), *a.ptrs(), _ptr(dq), _ptr(dk),
-                                 _ptr(dv), ctypes.c_void_p(_stream_int(stream, q.device))))
+                                 _ptr(dv), _stream_int(stream, q.device)))
 
 
 def fa_bwd_alibi(h, q, k, v, slopes, o, lse, d_o, dq, dk, dv, d_lse=None, prefix=None,
@@ -352,7 +349,7 @@ def fa_bwd_alibi(h, q, k, v, slopes, o, lse, d_o, dq, dk, dv, d_lse=None, prefix
     _check(load_library().fa_bwd_alibi(h, _ptr(q), _ptr(k), _ptr(v), _ptr(slopes), _ptr(o),
                                        _ptr(lse), _ptr(d_o), _ptr(d_lse), *a.ptrs(), _ptr(dq),
                                        _ptr(dk), _ptr(dv),
-                                       ctypes.c_void_p(_stream_int(stream, q.device))))
+                                       _stream_int(stream, q.device)))
 
 
 def fa_bwd_relbias(h, q, k, v, table, bucket_of, o, lse, d_o, dq, dk, dv, dtable, d_lse=None,
@@ -363,11 +360,13 @@ def fa_bwd_relbias(h, q, k, v, table, bucket_of, o, lse, d_o, dq, dk, dv, dtable
     _check(load_library().fa_bwd_relbias(h, _ptr(q), _ptr(k), _ptr(v), ctypes.byref(b), _ptr(o),
                                          _ptr(lse), _ptr(d_o), _ptr(d_lse), *a.ptrs(), _ptr(dq),
                                          _ptr(dk), _ptr(dv), _ptr(dtable),
-                                         ctypes.c_void_p(_stream_int(stream, q.device))))
+                                         _stream_int(stream, q.device)))
 
 
 def _stream_int(stream, device):
     import torch
+    if type(stream) is int:
+        return stream
     if stream is None:
         return torch.cuda.current_stream(device).cuda_stream
     if hasattr(stream, "cuda_stream"):
@@ -404,7 +403,7 @@ def fa_fwd_with_ranges(h, q, k, v, o, lse, atten_mask, ranges, stream=None):
     """fa_fwd for a dense-mask handle with the pre-pass's ranges supplied."""
     _check(load_library().fa_fwd_with_ranges(h, _ptr(q), _ptr(k), _ptr(v), _ptr(atten_mask),
                                              _ptr(ranges), _ptr(o), _ptr(lse),
-                                             ctypes.c_void_p(_stream_int(stream, q.device))))
+                                             _stream_int(stream, q.device)))
 
 
 def fa_fwd_paged(h, q, k_cache, v_cache, block_table, o, lse, actual_seq_qlen,
@@ -417,7 +416,7 @@ def fa_fwd_paged(h, q, k_cache, v_cache, block_table, o, lse, actual_seq_qlen,
     _check(load_library().fa_fwd_paged(h, _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                        _ptr(block_table), num_blocks, block_size, max_blocks,
                                        *a.ptrs(), _ptr(o), _ptr(lse),
-                                       ctypes.c_void_p(_stream_int(stream, q.device))))
+                                       _stream_int(stream, q.device)))
 
 
 def fa_fwd_noalloc(desc, q, k, v, o, lse, atten_mask=None, prefix=None, actual_seq_qlen=None,
@@ -541,16 +540,15 @@ class MaskedAttention:
                 FA_MASK_BNSS: (d.B, d.N, d.Sq, d.Skv)}.get(d.mask_kind)
 
     @staticmethod
-    def _need(device, **tensors):
-        """Each given as name=(tensor, dtypes, shape): contiguous, on `device`."""
+    def _need(device, shape, dtype, **tensors):
+        """Each given tensor: contiguous, of this dtype and shape, on `device`."""
         import torch
-        for name, (t, dtypes, shape) in tensors.items():
+        for name, t in tensors.items():
             if t is None:
                 continue
-            dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
-            if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_contiguous()
-                    or not t.is_cuda or t.device != device or tuple(t.shape) != tuple(shape)):
-                raise ValueError(f"{name} must be a contiguous {dtypes[0]} CUDA tensor of shape "
+            if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda
+                    or t.device != device or t.shape != shape or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape "
                                  f"{tuple(shape)} on {device}")
 
     def _need_bias(self, device, rel_bias, rel_buckets):
@@ -559,15 +557,17 @@ class MaskedAttention:
             raise ValueError("rel_bias needs rel_buckets, its bucket map")
         if not isinstance(rel_bias, torch.Tensor) or rel_bias.dim() != 2:
             raise ValueError("rel_bias must be a tensor [num_buckets, N]")
-        self._need(device, rel_bias=(rel_bias, torch.float32, (rel_bias.shape[0], self.desc.N)))
+        self._need(device, (rel_bias.shape[0], self.desc.N), torch.float32, rel_bias=rel_bias)
 
     @staticmethod
-    @contextlib.contextmanager
-    def _on(stream, device, *inputs):
-        """The tensors' device current, and `stream` (None: torch's current
-        one) current too, so that what is allocated belongs to it; tensors of
-        other streams are kept from reuse until this stream has read them."""
+    def _on(stream, device, inputs, body):
+        """body(raw stream) with the tensors' device current, and `stream`
+        (None: torch's current one) current too, so that what is allocated
+        belongs to it; tensors of other streams are kept from reuse until this
+        stream has read them."""
         import torch
+        if stream is None and torch.cuda.current_device() == device.index:
+            return body(torch.cuda.current_stream(device).cuda_stream)
         with torch.cuda.device(device):
             here = torch.cuda.current_stream(device)
             if stream is None:
@@ -575,11 +575,12 @@ class MaskedAttention:
             elif not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(int(stream), device=device)
             with torch.cuda.stream(stream):
-                yield stream
+                result = body(stream.cuda_stream)
             if stream != here:
                 for t in inputs:
                     if t is not None:
                         t.record_stream(stream)
+            return result
 
     def _relbias_forward(self, q, k, v, rel_bias, rel_buckets, atten_mask, ranges, slopes, prefix,
                          actual_seq_qlen, actual_seq_kvlen, out, lse, stream):
@@ -587,17 +588,20 @@ class MaskedAttention:
         if atten_mask is not None or ranges is not None or slopes is not None:
             raise ValueError("rel_bias goes with neither atten_mask, ranges nor slopes")
         oshape, lshape = self.out_shapes()
-        bf16, dev = torch.bfloat16, q.device
-        self._need(dev, q=(q, bf16, oshape), k=(k, bf16, self.kv_shape()),
-                   v=(v, bf16, self.kv_shape()), out=(out, bf16, oshape),
-                   lse=(lse, torch.float32, lshape))
+        bf16, f32, dev = torch.bfloat16, torch.float32, q.device
+        self._need(dev, oshape, bf16, q=q, out=out)
+        self._need(dev, self.kv_shape(), bf16, k=k, v=v)
+        self._need(dev, lshape, f32, lse=lse)
         self._need_bias(dev, rel_bias, rel_buckets)
-        with self._on(stream, dev, q, k, v, rel_bias, out, lse) as s:
-            out = torch.empty(oshape, dtype=bf16, device=dev) if out is None else out
-            lse = torch.empty(lshape, dtype=torch.float32, device=dev) if lse is None else lse
-            fa_fwd_relbias(self.handle, q, k, v, rel_bias, rel_buckets, out, lse, prefix,
+
+        def body(s):
+            o = torch.empty_like(q) if out is None else out
+            l = torch.empty(lshape, dtype=f32, device=dev) if lse is None else lse
+            fa_fwd_relbias(self.handle, q, k, v, rel_bias, rel_buckets, o, l, prefix,
                            actual_seq_qlen, actual_seq_kvlen, s)
-        return out, lse
+            return o, l
+
+        return self._on(stream, dev, (q, k, v, rel_bias, out, lse), body)
 
     def backward(self, d_o, q, k, v, o, lse, atten_mask=None, prefix=None, actual_seq_qlen=None,
                  actual_seq_kvlen=None, d_lse=None, slopes=None, rel_bias=None, rel_buckets=None,
@@ -608,37 +612,39 @@ class MaskedAttention:
         None: 0)."""
         import torch
         oshape, lshape = self.out_shapes()
-        kshape = self.kv_shape()
         bf16, f32, dev = torch.bfloat16, torch.float32, q.device
-        self._need(dev, q=(q, bf16, oshape), k=(k, bf16, kshape), v=(v, bf16, kshape),
-                   o=(o, bf16, oshape), d_o=(d_o, bf16, oshape), lse=(lse, f32, lshape),
-                   d_lse=(d_lse, f32, lshape), dq=(dq, bf16, oshape), dk=(dk, bf16, kshape),
-                   dv=(dv, bf16, kshape), slopes=(slopes, f32, (self.desc.N,)))
+        self._need(dev, oshape, bf16, q=q, o=o, d_o=d_o, dq=dq)
+        self._need(dev, self.kv_shape(), bf16, k=k, v=v, dk=dk, dv=dv)
+        self._need(dev, lshape, f32, lse=lse, d_lse=d_lse)
+        if slopes is not None:
+            self._need(dev, (self.desc.N,), f32, slopes=slopes)
         if atten_mask is not None and self._mask_shape() is not None:
-            self._need(dev, atten_mask=(atten_mask, (torch.uint8, torch.bool), self._mask_shape()))
+            kind = atten_mask.dtype if atten_mask.dtype is torch.bool else torch.uint8
+            self._need(dev, self._mask_shape(), kind, atten_mask=atten_mask)
         if rel_bias is not None:
             if atten_mask is not None or slopes is not None:
                 raise ValueError("rel_bias goes with neither atten_mask nor slopes")
             self._need_bias(dev, rel_bias, rel_buckets)
-            self._need(dev, d_rel_bias=(d_rel_bias, f32, rel_bias.shape))
-        with self._on(stream, dev, d_o, q, k, v, o, lse, atten_mask, d_lse, slopes, rel_bias, dq, dk,
-                      dv, d_rel_bias) as s:
-            dq = torch.empty(oshape, dtype=bf16, device=dev) if dq is None else dq
-            dk = torch.empty(kshape, dtype=bf16, device=dev) if dk is None else dk
-            dv = torch.empty(kshape, dtype=bf16, device=dev) if dv is None else dv
-            lens = dict(d_lse=d_lse, prefix=prefix, actual_seq_qlen=actual_seq_qlen,
-                        actual_seq_kvlen=actual_seq_kvlen, stream=s)
+            self._need(dev, rel_bias.shape, f32, d_rel_bias=d_rel_bias)
+
+        def body(s):
+            gq = torch.empty_like(q) if dq is None else dq
+            gk = torch.empty_like(k) if dk is None else dk
+            gv = torch.empty_like(v) if dv is None else dv
+            lens = (d_lse, prefix, actual_seq_qlen, actual_seq_kvlen, s)
             if rel_bias is not None:
-                if d_rel_bias is None:
-                    d_rel_bias = torch.empty(rel_bias.shape, dtype=f32, device=dev)
-                fa_bwd_relbias(self.handle, q, k, v, rel_bias, rel_buckets, o, lse, d_o, dq, dk,
-                               dv, d_rel_bias, **lens)
-                return dq, dk, dv, d_rel_bias
+                gt = torch.empty_like(rel_bias) if d_rel_bias is None else d_rel_bias
+                fa_bwd_relbias(self.handle, q, k, v, rel_bias, rel_buckets, o, lse, d_o, gq, gk,
+                               gv, gt, *lens)
+                return gq, gk, gv, gt
             if slopes is not None:
-                fa_bwd_alibi(self.handle, q, k, v, slopes, o, lse, d_o, dq, dk, dv, **lens)
+                fa_bwd_alibi(self.handle, q, k, v, slopes, o, lse, d_o, gq, gk, gv, *lens)
             else:
-                fa_bwd(self.handle, q, k, v, o, lse, d_o, dq, dk, dv, atten_mask=atten_mask, **lens)
-        return dq, dk, dv
+                fa_bwd(self.handle, q, k, v, o, lse, d_o, gq, gk, gv, atten_mask, *lens)
+            return gq, gk, gv
+
+        return self._on(stream, dev, (d_o, q, k, v, o, lse, atten_mask, d_lse, slopes, rel_bias, dq,
+                                      dk, dv, d_rel_bias), body)
 
     def paged(self, q, k_cache, v_cache, block_table, actual_seq_qlen, actual_seq_kvlen,
               prefix=None, out=None, lse=None, stream=None):

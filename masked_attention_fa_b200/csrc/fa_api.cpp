@@ -422,8 +422,11 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
     p.alibi = d->alibi;
   }
   if (bias) {
-    st = prepare_rel(h, bias, stream, &p.rel);
+    RelTable table;
+    st = prepare_rel(h, bias, stream, &p.rel, &table);
     if (st != FA_OK) return st;
+    const cudaError_t er = launch_rel_expand(table, stream);
+    if (er != cudaSuccess) return cuda_fail(er, "bias expansion launch");
   }
   p.tnd = d->layout == FA_TND ? 1 : 0;
   p.scale_log2 = (float)(d->scale * 1.4426950408889634073599);

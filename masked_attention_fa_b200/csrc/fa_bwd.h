@@ -61,9 +61,15 @@ FA_HD TileRange key_tile_rows(const SeqRec& s, int64_t c0) {
 // inside (-reach, reach) reaches up to 254 past either end).
 FA_HD int32_t rel_width(int32_t reach) { return 2 * reach + 1 + 2 * kRelPad; }
 
-// Expand table [num_buckets][N] into ext.
-cudaError_t launch_rel_expand(const float* table, const int32_t* bucket_of, float* ext, int32_t N,
-                              int32_t num_buckets, int32_t reach, cudaStream_t stream);
+// A bias table and its copy by distance (see RelBias).
+struct RelTable {
+  const float* table;        // [num_buckets][N]
+  const int32_t* bucket_of;  // device, [2 reach + 1]
+  float* ext;                // out: [N][4][rel_row(reach)]
+  int32_t N, reach;
+};
+// Lays the table out by distance.
+cudaError_t launch_rel_expand(const RelTable& t, cudaStream_t stream);
 
 // ------------------------------------------------------------- the backward
 struct __align__(64) BwdParams {
@@ -89,9 +95,11 @@ struct __align__(64) BwdParams {
   void* dv;
   const float* slopes;       // ALiBi, else null
   RelBias rel;
+  RelTable rel_table;        // source of rel.ext, laid out with the row statistics
   // Gradient of the bias by distance: one row of rel_width sums per query
   // tile (indexed by its statistics block), else null.
   float* rel_part;
+  unsigned int* rel_done;    // [N] counters of launch_rel_reduce, set to 0 with the statistics
   int64_t q_sb, q_sh, q_st;  // element strides of Q, O and their gradients
   int64_t k_sb, k_sh, k_st;  // of K, V and their gradients
   int64_t l_sb, l_sh;        // of lse
@@ -103,7 +111,8 @@ struct __align__(64) BwdParams {
   uint64_t timeout_ns;
 };
 
-// Row statistics of every query tile (see BwdParams::stats).
+// Row statistics of every query tile (see BwdParams::stats), and with a bias
+// its layout by distance.
 cudaError_t launch_bwd_stats(int D, const BwdParams& p, cudaStream_t stream);
 // dQ (and rel_part), then dK and dV.
 cudaError_t launch_bwd(int D, const BwdParams& p, int num_sms, cudaStream_t stream,
@@ -123,9 +132,9 @@ cudaError_t launch_bwd_ranges(const BwdOccParams& a, cudaStream_t stream);
 
 // dtable[c][h] = the sum of rel_part over head h's query tiles (rows
 // [h * tiles, (h + 1) * tiles) of rel_part) and the distances of bucket c, in
-// a fixed order. dist: scratch, fp64 [N][rel_width].
-cudaError_t launch_rel_reduce(const float* rel_part, double* dist, const int32_t* bucket_of,
-                              float* dtable, int32_t N, int32_t tiles, int32_t num_buckets,
-                              int32_t reach, cudaStream_t stream);
+// a fixed order. dist: scratch, fp64 [N][rel_width]; done: [N], 0.
+cudaError_t launch_rel_reduce(const float* rel_part, double* dist, unsigned int* done,
+                              const int32_t* bucket_of, float* dtable, int32_t N, int32_t tiles,
+                              int32_t num_buckets, int32_t reach, cudaStream_t stream);
 
 }  // namespace fa

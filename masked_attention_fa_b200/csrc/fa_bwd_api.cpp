@@ -72,8 +72,8 @@ fa_status_t validate_rel(const fa_desc_t* d, const fa_relbias_t* bias) {
   return FA_OK;
 }
 
-fa_status_t prepare_rel(fa_handle_t h, const fa_relbias_t* bias, cudaStream_t stream,
-                        RelBias* out) {
+fa_status_t prepare_rel(fa_handle_t h, const fa_relbias_t* bias, cudaStream_t stream, RelBias* out,
+                        RelTable* table) {
   const int32_t N = (int32_t)h->desc.N, R = bias->reach, row = rel_row(R);
   if (h->any_call) {  // an earlier call on another stream may still read the tables
     const cudaError_t e = cudaStreamWaitEvent(stream, h->last_call, 0);
@@ -94,10 +94,8 @@ fa_status_t prepare_rel(fa_handle_t h, const fa_relbias_t* bias, cudaStream_t st
     held.assign(bias->bucket_of, bias->bucket_of + entries);
   }
   float* ext = static_cast<float*>(h->rel.ext.ptr);
-  const cudaError_t e = launch_rel_expand(bias->table, static_cast<const int32_t*>(h->rel.map.ptr),
-                                          ext, N, bias->num_buckets, R, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "bias expansion launch");
   *out = RelBias{ext, R, row};
+  *table = RelTable{bias->table, static_cast<const int32_t*>(h->rel.map.ptr), ext, N, R};
   return FA_OK;
 }
 
@@ -230,15 +228,17 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   if (st != FA_OK) return st;
   const BwdState& bw = h->bwd;
 
-  // Scratch: row statistics | bias sums by tile and by distance | the dense
-  // mask's ranges and classes.
+  // Scratch: row statistics | bias sums by tile and by distance, counters | the
+  // dense mask's ranges and classes.
   const size_t stat_bytes = align_up((size_t)bw.tiles * d->N * 256 * sizeof(float), 256);
   const size_t W = a.bias ? (size_t)rel_width(a.bias->reach) : 0;
   const size_t part_bytes = align_up((size_t)bw.tiles * d->N * W * sizeof(float), 256);
   const size_t dist_bytes = align_up((size_t)d->N * W * sizeof(double), 256);
   const int64_t planes = mask_planes(d, has_mask);
   const size_t occ_bytes = planes ? occupancy_bytes(planes, d->Sq, d->Skv) : 0;
-  st = ensure_buffer(h, &h->bwd.scratch, stat_bytes + part_bytes + dist_bytes + occ_bytes);
+  const size_t done_bytes = a.bias ? align_up((size_t)d->N * sizeof(unsigned int), 256) : 0;
+  st = ensure_buffer(h, &h->bwd.scratch,
+                     stat_bytes + part_bytes + dist_bytes + done_bytes + occ_bytes);
   if (st != FA_OK) return st;
   uint8_t* scratch = static_cast<uint8_t*>(bw.scratch.ptr);
   uint8_t* lists = static_cast<uint8_t*>(bw.lists.ptr);
@@ -292,8 +292,9 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
       return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled failed for operand %d", i);
   }
   if (a.bias) {
-    st = prepare_rel(h, a.bias, stream, &p.rel);
+    st = prepare_rel(h, a.bias, stream, &p.rel, &p.rel_table);
     if (st != FA_OK) return st;
+    p.rel_done = reinterpret_cast<unsigned int*>(scratch + stat_bytes + part_bytes + dist_bytes);
     p.rel_part = reinterpret_cast<float*>(scratch + stat_bytes);
   }
   if (has_mask) {
@@ -307,7 +308,7 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
       std::memset(&oc, 0, sizeof(oc));
       occupancy_shape(&oc, bw.geo0, planes);
       oc.mask = a.atten_mask;
-      uint8_t* occ = scratch + stat_bytes + part_bytes + dist_bytes;
+      uint8_t* occ = scratch + stat_bytes + part_bytes + dist_bytes + done_bytes;
       oc.ranges = reinterpret_cast<TileRange*>(occ);
       oc.cls = occ + align_up((size_t)(oc.n_planes * oc.n_qt) * sizeof(TileRange), 256);
       e = launch_occupancy(oc, h->num_sms, stream);
@@ -337,9 +338,12 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
     return cuda_fail(e, "backward launch");
   }
   if (a.bias) {
-    e = launch_rel_reduce(p.rel_part, reinterpret_cast<double*>(scratch + stat_bytes + part_bytes),
-                          static_cast<const int32_t*>(h->rel.map.ptr), a.dtable, (int32_t)d->N,
-                          bw.tiles, a.bias->num_buckets, a.bias->reach, stream);
+    if (bw.n_q > 0)
+      e = launch_rel_reduce(p.rel_part, reinterpret_cast<double*>(scratch + stat_bytes + part_bytes),
+                            p.rel_done, p.rel_table.bucket_of, a.dtable, (int32_t)d->N, bw.tiles,
+                            a.bias->num_buckets, a.bias->reach, stream);
+    else
+      e = cudaMemsetAsync(a.dtable, 0, (size_t)a.bias->num_buckets * d->N * sizeof(float), stream);
     if (e != cudaSuccess) return cuda_fail(e, "bias gradient launch");
   }
   e = cudaEventRecord(h->last_call, stream);

@@ -25,10 +25,34 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return s;
 }
 
+// Entries [256 chunk, 256 chunk + 256) of the four copies of head h.
+__device__ __forceinline__ void expand_chunk(const RelTable& t, int h, int chunk) {
+  const int row = rel_row(t.reach);
+  const int x = chunk * 256 + threadIdx.x;
+  if (x >= row) return;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int rel = min(max(x + s - t.reach - kRelPad, -t.reach), t.reach);
+    t.ext[((int64_t)h * 4 + s) * row + x] =
+        t.table[(int64_t)t.bucket_of[rel + t.reach] * t.N + h] * kLog2e;
+  }
+}
+
+__global__ void __launch_bounds__(256) rel_expand(RelTable t) { expand_chunk(t, blockIdx.y, blockIdx.x); }
+
 // One CTA per query tile, D / 8 threads per row (16-byte loads, whole rows
 // per group of threads): delta_i = sum_d do_id o_id.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_stats(const __grid_constant__ BwdParams p) {
+  // The query walk may set itself up meanwhile.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if ((int)blockIdx.x >= p.n_q) {  // the CTAs past the query tiles lay the bias out
+    const int x = blockIdx.x - p.n_q, chunks = (rel_row(p.rel_table.reach) + 255) / 256;
+    if (x == 0)
+      for (int h = threadIdx.x; h < p.rel_table.N; h += 256) p.rel_done[h] = 0u;
+    expand_chunk(p.rel_table, x / chunks, x % chunks);
+    return;
+  }
   constexpr int L = D / 8;            // threads per row
   constexpr int R = 256 / L;          // rows per pass
   const BwdItem it = p.q_items[blockIdx.x];
@@ -115,26 +139,21 @@ __global__ void __launch_bounds__(256) bwd_ranges(BwdOccParams a, int q_blocks) 
   a.k_items[n] = it;
 }
 
-__global__ void __launch_bounds__(256) rel_expand(const float* __restrict__ table,
+// dist[h][e] = sum over head h's query tiles, in 64 bits: one CTA per head and
+// 32 distances, warp w adds tiles w, w + 8, ... and the eight sums are added
+// in warp order. The last CTA of a head to finish then sums the distances of
+// each bucket, those past the reach with the end they clip to: one warp per
+// bucket. Every order is fixed.
+__global__ void __launch_bounds__(256) rel_reduce(const float* __restrict__ part, double* dist,
+                                                  unsigned int* done,
                                                   const int32_t* __restrict__ bucket_of,
-                                                  float* __restrict__ ext, int N, int num_buckets,
-                                                  int reach, int row) {
-  const int h = blockIdx.y;
-  const int x = blockIdx.x * 256 + threadIdx.x;
-  if (x >= row) return;
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int rel = min(max(x + s - reach - kRelPad, -reach), reach);
-    ext[((int64_t)h * 4 + s) * row + x] = table[(int64_t)bucket_of[rel + reach] * N + h] * kLog2e;
-  }
-}
-
-// First step: dist[h][e] = sum over head h's query tiles, in 64 bits. One CTA
-// per head and 32 distances; warp w adds tiles w, w + 8, ... and the eight
-// sums are added in warp order.
-__global__ void __launch_bounds__(256) rel_sum_tiles(const float* __restrict__ part,
-                                                     double* __restrict__ dist, int tiles, int W) {
+                                                  float* __restrict__ dtable, int N, int tiles,
+                                                  int reach, int num_buckets) {
   __shared__ double sm[8][32];
+  __shared__ double by_dist[2 * kRelMaxReach + 1 + 2 * kRelPad];
+  __shared__ int32_t bucket[2 * kRelMaxReach + 1 + 2 * kRelPad];
+  __shared__ bool last;
+  const int W = rel_width(reach);
   const int h = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = blockIdx.x * 32 + lane;
   double s = 0.0;
@@ -142,37 +161,42 @@ __global__ void __launch_bounds__(256) rel_sum_tiles(const float* __restrict__ p
     for (int t = w; t < tiles; t += 8) s += part[((int64_t)h * tiles + t) * W + d];
   sm[w][lane] = s;
   __syncthreads();
-  if (w == 0 && d < W) {
-    double a = sm[0][lane];
-    for (int x = 1; x < 8; ++x) a += sm[x][lane];
-    dist[(int64_t)h * W + d] = a;
+  if (w == 0) {
+    if (d < W) {
+      double a = sm[0][lane];
+      for (int x = 1; x < 8; ++x) a += sm[x][lane];
+      dist[(int64_t)h * W + d] = a;
+    }
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) last = atomicAdd(done + h, 1u) == gridDim.x - 1;
   }
-}
-
-// Second step: one warp per (bucket, head) adds the distances of its bucket,
-// those past the reach with the end they clip to.
-__global__ void __launch_bounds__(256) rel_sum_buckets(const double* __restrict__ dist,
-                                                       const int32_t* __restrict__ bucket_of,
-                                                       float* __restrict__ dtable, int N, int W,
-                                                       int reach, int num_buckets) {
-  const int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (n >= (int64_t)num_buckets * N) return;
-  const int c = (int)(n / N), h = (int)(n % N);
-  double s = 0.0;
-  for (int e = lane; e < W; e += 32)
-    if (bucket_of[min(max(e - kRelPad, 0), 2 * reach)] == c) s += dist[(int64_t)h * W + e];
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int e = threadIdx.x; e < W; e += 256) {
+    by_dist[e] = __ldcg(dist + (int64_t)h * W + e);
+    bucket[e] = bucket_of[min(max(e - kRelPad, 0), 2 * reach)];
+  }
+  __syncthreads();
+  for (int c = w; c < num_buckets; c += 8) {
+    double a = 0.0;
+    for (int e = lane; e < W; e += 32)
+      if (bucket[e] == c) a += by_dist[e];
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-  if (lane == 0) dtable[n] = (float)s;
+    for (int x = 16; x > 0; x >>= 1) a += __shfl_xor_sync(0xffffffffu, a, x);
+    if (lane == 0) dtable[(int64_t)c * N + h] = (float)a;
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_bwd_stats(int D, const BwdParams& p, cudaStream_t stream) {
   if (p.n_q <= 0) return cudaSuccess;
-  if (D == 128) bwd_stats<128><<<p.n_q, 256, 0, stream>>>(p);
-  else bwd_stats<64><<<p.n_q, 256, 0, stream>>>(p);
+  const int grid =
+      p.n_q + (p.rel.ext ? (rel_row(p.rel_table.reach) + 255) / 256 * p.rel_table.N : 0);
+  if (D == 128) bwd_stats<128><<<grid, 256, 0, stream>>>(p);
+  else bwd_stats<64><<<grid, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -182,21 +206,16 @@ cudaError_t launch_bwd_ranges(const BwdOccParams& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_rel_expand(const float* table, const int32_t* bucket_of, float* ext, int32_t N,
-                              int32_t num_buckets, int32_t reach, cudaStream_t stream) {
-  const int row = rel_row(reach);
-  rel_expand<<<dim3((row + 255) / 256, N), 256, 0, stream>>>(table, bucket_of, ext, N, num_buckets,
-                                                             reach, row);
+cudaError_t launch_rel_expand(const RelTable& t, cudaStream_t stream) {
+  rel_expand<<<dim3((rel_row(t.reach) + 255) / 256, t.N), 256, 0, stream>>>(t);
   return cudaGetLastError();
 }
 
-cudaError_t launch_rel_reduce(const float* rel_part, double* dist, const int32_t* bucket_of,
-                              float* dtable, int32_t N, int32_t tiles, int32_t num_buckets,
-                              int32_t reach, cudaStream_t stream) {
-  const int W = rel_width(reach);
-  rel_sum_tiles<<<dim3((W + 31) / 32, N), 256, 0, stream>>>(rel_part, dist, tiles, W);
-  rel_sum_buckets<<<(int)(((int64_t)num_buckets * N + 7) / 8), 256, 0, stream>>>(
-      dist, bucket_of, dtable, N, W, reach, num_buckets);
+cudaError_t launch_rel_reduce(const float* rel_part, double* dist, unsigned int* done,
+                              const int32_t* bucket_of, float* dtable, int32_t N, int32_t tiles,
+                              int32_t num_buckets, int32_t reach, cudaStream_t stream) {
+  rel_reduce<<<dim3((rel_width(reach) + 31) / 32, N), 256, 0, stream>>>(
+      rel_part, dist, done, bucket_of, dtable, N, tiles, reach, num_buckets);
   return cudaGetLastError();
 }
 

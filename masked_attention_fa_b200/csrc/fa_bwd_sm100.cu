@@ -38,6 +38,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "../../include/fa.h"
@@ -970,9 +971,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
   float* sSum = reinterpret_cast<float*>(sStat + C::kStatBytes);
   auto* ctl = reinterpret_cast<BCtl*>(sStat + C::kStatBytes + C::kSumBytes);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-  // The two walks need nothing of each other: the next launch of the stream
-  // may take each SM this one leaves.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) atomicOr(p.err_word, kErrTimeout | (kBSiteSmem << kErrWhereShift));
     return;
@@ -1020,6 +1018,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+  if constexpr (!kKeys) {
+    // What is above ran beside the row statistics' kernel; what is below reads
+    // them. The two walks need nothing of each other: from here on the key
+    // walk may take each SM that is free.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
   const WaitCtx w{&ctl->abort_flag, p.err_word, p.timeout_ns};
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwdRegsMath));
@@ -1053,25 +1058,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
 // ----------------------------------------------------------------- host
 
 template <int D, bool kKeys, int kBias>
-static cudaError_t launch_walk(const BwdParams& p, int grid, bool beside, cudaStream_t stream,
+static cudaError_t launch_walk(const BwdParams& p, int grid, bool early, cudaStream_t stream,
                                const char** why) {
   using C = dev::BCfg<D, kKeys>;
   auto kern = dev::fa_bwd_sm100<D, kKeys, kBias>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)C::kSmemBytes);
+  // Devices on which the kernel's attributes are set (one bit each).
+  static std::atomic<uint64_t> configured{0};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
-  static int regs = 0;  // the same on every device: one architecture
-  if (regs == 0) {
+  const uint64_t bit = device < 64 ? 1ull << device : 0ull;
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
+    if (e != cudaSuccess) return e;
     cudaFuncAttributes attr;
     e = cudaFuncGetAttributes(&attr, kern);
     if (e != cudaSuccess) return e;
-    regs = attr.numRegs;
-  }
-  // setmaxnreg redistributes the registers the CTA was launched with; a split
-  // larger than that allocation would never be granted.
-  if (regs < 128) {
-    if (why) *why = "kernel compiled with fewer registers than its warpgroup split needs";
-    return cudaErrorInvalidConfiguration;
+    // setmaxnreg redistributes the registers the CTA was launched with; a split
+    // larger than that allocation would never be granted.
+    if (attr.numRegs < 128) {
+      if (why) *why = "kernel compiled with fewer registers than its warpgroup split needs";
+      return cudaErrorInvalidConfiguration;
+    }
+    configured.fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -1082,7 +1091,7 @@ static cudaError_t launch_walk(const BwdParams& p, int grid, bool beside, cudaSt
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = beside ? 1 : 0;
+  cfg.numAttrs = early ? 1 : 0;  // may start before the launch ahead of it ends
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -1090,7 +1099,7 @@ template <int D, int kBias>
 static cudaError_t launch_both(const BwdParams& p, int num_sms, cudaStream_t stream,
                                const char** why) {
   if (p.n_q > 0) {
-    const cudaError_t e = launch_walk<D, false, kBias>(p, p.n_q < num_sms ? p.n_q : num_sms, false,
+    const cudaError_t e = launch_walk<D, false, kBias>(p, p.n_q < num_sms ? p.n_q : num_sms, true,
                                                        stream, why);
     if (e != cudaSuccess) return e;
   }

@@ -96,9 +96,10 @@ fa_status_t ensure_buffer(fa_handle_t h, DeviceBuffer* buf, size_t bytes);
 fa_status_t refuse_capture(cudaStream_t stream);
 // Frees what the backward and the relative position bias hold.
 void release_training(fa_handle_t h);
-// Lays the bias out by distance on `stream` (see RelBias) for this call.
-fa_status_t prepare_rel(fa_handle_t h, const fa_relbias_t* bias, cudaStream_t stream,
-                        RelBias* out);
+// The handle's copy of the bias by distance (see RelBias) and what lays it out
+// for this call: launch_rel_expand(*table), or the row statistics' launch.
+fa_status_t prepare_rel(fa_handle_t h, const fa_relbias_t* bias, cudaStream_t stream, RelBias* out,
+                        RelTable* table);
 fa_status_t validate_rel(const fa_desc_t* d, const fa_relbias_t* bias);
 int64_t mask_planes(const fa_desc_t* d, int has_mask);
 std::vector<int64_t> make_key(const fa_desc_t* d, const int64_t* prefix, const int64_t* cu_q,
