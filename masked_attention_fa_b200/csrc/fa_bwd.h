@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -22,8 +23,18 @@ struct BwdItem {
   int32_t stat;  // row-statistics block: the tile's own (query list), or that
                  // of the (sequence, head)'s query tile 0 (key list)
   int32_t lo, hi, full_lo, full_hi;
+  int32_t span;  // key list: this key tile's KeySpan; dQ list: that of key tile 0
+  int32_t pad[3];
 };
-static_assert(sizeof(BwdItem) == 32, "BwdItem layout");
+static_assert(sizeof(BwdItem) == 48, "BwdItem layout");
+
+// Where the key walk writes the dS of a key tile: the tile of dS of query tile
+// t in [lo, hi) is first + t. One per key tile, [h][key tiles of all
+// sequences].
+struct KeySpan {
+  int32_t first, lo, hi, pad;
+};
+static_assert(sizeof(KeySpan) == 16, "KeySpan layout");
 
 // Query tiles that see keys [c0, c0 + 128) of sequence s: [lo, hi) holds
 // every tile with a visible pair; in [full_lo, full_hi) every stored row sees
@@ -77,6 +88,10 @@ struct __align__(64) BwdParams {
   const SeqRec* seqs;
   const BwdItem* q_items;
   const BwdItem* k_items;
+  const BwdItem* g_items;    // two query tiles each, for the dQ kernel
+  const KeySpan* spans;
+  // dS in bf16 (see launch_bwd), or null: tiles of [16][128 keys][8 queries].
+  __nv_bfloat16* ds;
   // Row statistics, one block of 2 x 128 floats per query tile: the negated
   // lse in log2 units (-inf for rows that see no key or are not stored, so
   // that their weights are 0 without a mask), then dlse - delta.
@@ -96,8 +111,8 @@ struct __align__(64) BwdParams {
   const float* slopes;       // ALiBi, else null
   RelBias rel;
   RelTable rel_table;        // source of rel.ext, laid out with the row statistics
-  // Gradient of the bias by distance: one row of rel_width sums per query
-  // tile (indexed by its statistics block), else null.
+  // Gradient of the bias by distance: one row of rel_width sums per key tile
+  // (indexed by its span), else null.
   float* rel_part;
   unsigned int* rel_done;    // [N] counters of launch_rel_reduce, set to 0 with the statistics
   int64_t q_sb, q_sh, q_st;  // element strides of Q, O and their gradients
@@ -105,7 +120,7 @@ struct __align__(64) BwdParams {
   int64_t l_sb, l_sh;        // of lse
   int64_t m_sb, m_sh, m_si;  // of the mask
   int32_t alibi;             // fa_alibi_t
-  int32_t n_q, n_k;          // items
+  int32_t n_q, n_k, n_g;     // items
   int32_t tnd;
   float scale, scale_log2;
   uint64_t timeout_ns;
@@ -114,23 +129,34 @@ struct __align__(64) BwdParams {
 // Row statistics of every query tile (see BwdParams::stats), and with a bias
 // its layout by distance.
 cudaError_t launch_bwd_stats(int D, const BwdParams& p, cudaStream_t stream);
-// dQ (and rel_part), then dK and dV.
+// dQ, dK, dV and rel_part.
+//
+// Without p.ds by two walks that need nothing of each other: dQ by query tiles
+// (S, dP, dQ), dK and dV by key tiles (S, dP, dV, dK): seven products a pair
+// of tiles. With p.ds the key walk also writes dS to memory, 32 KB a pair of
+// tiles, and a third kernel multiplies it by K: five products. The matrix
+// products run into the card's power limit, so at head dim 128 two products
+// less are worth the memory traffic once there is enough work (the host's rule
+// and what it measured: refresh_lists).
 cudaError_t launch_bwd(int D, const BwdParams& p, int num_sms, cudaStream_t stream,
                        const char** why);
 
 // Dense masks: copies the occupancy pre-pass's key-tile ranges into the
-// query items and reduces its classes to the key items' query-tile ranges.
+// query items (and their union to the dQ kernel's items) and reduces its
+// classes to the key items' query-tile ranges and spans.
 struct BwdOccParams {
   const TileRange* ranges;  // [plane][n_qt]
   const uint8_t* cls;       // [plane][n_qt][n_kt]
   BwdItem* q_items;
   BwdItem* k_items;
+  BwdItem* g_items;
+  KeySpan* spans;
   int64_t occ_sb, occ_sh;   // plane = b * occ_sb + h * occ_sh
-  int32_t n_q, n_k, n_qt, n_kt;
+  int32_t n_q, n_k, n_g, n_qt, n_kt;
 };
 cudaError_t launch_bwd_ranges(const BwdOccParams& a, cudaStream_t stream);
 
-// dtable[c][h] = the sum of rel_part over head h's query tiles (rows
+// dtable[c][h] = the sum of rel_part over head h's key tiles (rows
 // [h * tiles, (h + 1) * tiles) of rel_part) and the distances of bucket c, in
 // a fixed order. dist: scratch, fp64 [N][rel_width]; done: [N], 0.
 cudaError_t launch_rel_reduce(const float* rel_part, double* dist, unsigned int* done,

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <cstring>
 #include <exception>
 #include <vector>
@@ -46,7 +47,7 @@ fa_status_t refuse_capture(cudaStream_t stream) {
 }
 
 void release_training(fa_handle_t h) {
-  for (DeviceBuffer* b : {&h->bwd.lists, &h->bwd.scratch, &h->rel.map, &h->rel.ext})
+  for (DeviceBuffer* b : {&h->bwd.lists, &h->bwd.scratch, &h->bwd.spill, &h->rel.map, &h->rel.ext})
     if (b->ptr) cudaFree(b->ptr);
 }
 
@@ -103,13 +104,22 @@ fa_status_t prepare_rel(fa_handle_t h, const fa_relbias_t* bias, cudaStream_t st
 
 namespace {
 
-// Longest first, in buckets of similar length inside which the items of one
-// (sequence, head) stand together: the tiles in flight then share their
-// operands through L2 (see order_work_list).
-void order_items(std::vector<BwdItem>* items, bool locality) {
-  const int32_t bucket = locality ? kLocalityTiles : 1;
-  std::sort(items->begin(), items->end(), [bucket](const BwdItem& a, const BwdItem& c) {
+// At most 4 GiB of dS are held at once (the test hook makes it less).
+int64_t spill_tiles() {
+  if (const char* t = std::getenv("FA_TEST_SPILL_TILES")) return std::atoll(t);
+  return (int64_t(4) << 30) / (128 * 128 * 2);
+}
+
+// Items without a tile first (their zeros are written beside the first items'
+// products), then longest first, in buckets of similar length inside which the
+// items of one (sequence, head) stand together: the tiles in flight then share
+// their operands through L2 (see order_work_list).
+void order_items(std::vector<BwdItem>::iterator first, std::vector<BwdItem>::iterator last,
+                 int num_sms) {
+  const int32_t bucket = claims_items(last - first, num_sms) ? kLocalityTiles : 1;
+  std::sort(first, last, [bucket](const BwdItem& a, const BwdItem& c) {
     const int32_t la = a.hi - a.lo, lc = c.hi - c.lo;
+    if ((la <= 0) != (lc <= 0)) return la <= 0;
     const int32_t ba = (la + bucket - 1) / bucket, bc = (lc + bucket - 1) / bucket;
     if (ba != bc) return ba > bc;
     if (a.b != c.b) return a.b < c.b;
@@ -125,6 +135,7 @@ fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* c
                           const int64_t* cu_kv, int has_mask, cudaStream_t stream) {
   BwdState& bw = h->bwd;
   std::vector<int64_t> key = make_key(&h->desc, prefix, cu_q, cu_kv, has_mask);
+  key.push_back(bw.no_spill);
   if (bw.valid && key == bw.key) return FA_OK;
   const std::vector<SeqRec> recs = decode_geometry(&h->desc, prefix, cu_q, cu_kv, has_mask);
   const int32_t N = (int32_t)h->desc.N;
@@ -135,40 +146,93 @@ fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* c
   }
   if (std::max(tiles, k_tiles) * N > 0x3fffffff)
     return fail(FA_ERR_UNSUPPORTED, "too many work items");
-  std::vector<BwdItem> qi, ki;
+  // Two products less against 32 KB written and read a pair of tiles, and one
+  // after the other instead of side by side. Causal, D = 128: 16 heads x 2048
+  // (512 items) 71 us with dS written, 68 by two walks, 8 heads x 2048 60 and
+  // 45, but 32 heads x 2048 (1,024 items) 136 and 149, 32 x 4096 430 and 459.
+  // At D = 64 the products weigh half: 651 and 610 us on the bias backward of
+  // 32 heads x 4096.
+  bool spill = !bw.no_spill && h->desc.D == 128 && (tiles + k_tiles) * N > 4 * h->num_sms;
+  const int64_t cap = spill_tiles();
+  std::vector<BwdItem> qi, ki, gi;
+  std::vector<KeySpan> spans((size_t)(k_tiles * N));
   qi.reserve((size_t)(tiles * N));
   ki.reserve((size_t)(k_tiles * N));
-  int64_t base = 0;
+  std::vector<BwdState::Chunk> chunks;
+  int64_t q_base = 0, k_base = 0, used = 0;  // used: tiles of dS in the current chunk
   for (size_t b = 0; b < recs.size(); ++b) {
     const SeqRec& s = recs[b];
     const int32_t nq = (s.sq + kTileM - 1) / kTileM, nk = (s.skv + kTileN - 1) / kTileN;
-    for (int32_t t = 0; t < nq; ++t) {
-      const TileRange r = tile_range(s, (int64_t)t * kTileM);
-      for (int32_t hd = 0; hd < N; ++hd)
-        qi.push_back(BwdItem{(int32_t)b, hd, t, (int32_t)(hd * tiles + base + t), r.lo, r.hi,
-                             r.full_lo, r.full_hi});
-    }
+    std::vector<TileRange> qr((size_t)nq), kr((size_t)nk);
+    for (int32_t t = 0; t < nq; ++t) qr[t] = tile_range(s, (int64_t)t * kTileM);
+    int64_t need = 0;  // tiles of dS of one head; a mask's are not known here
     for (int32_t t = 0; t < nk; ++t) {
-      const TileRange r = key_tile_rows(s, (int64_t)t * kTileN);
-      for (int32_t hd = 0; hd < N; ++hd)
-        ki.push_back(BwdItem{(int32_t)b, hd, t, (int32_t)(hd * tiles + base), r.lo, r.hi, r.full_lo,
-                             r.full_hi});
+      kr[t] = key_tile_rows(s, (int64_t)t * kTileN);
+      need += has_mask ? nq : kr[t].hi - kr[t].lo;
     }
-    base += nq;
+    if (need > cap) spill = false;
+    for (int32_t hd = 0; hd < N; ++hd) {
+      for (int32_t t = 0; t < nq; ++t)
+        qi.push_back(BwdItem{(int32_t)b, hd, t, (int32_t)(hd * tiles + q_base + t), qr[t].lo,
+                             qr[t].hi, qr[t].full_lo, qr[t].full_hi, 0, {0, 0, 0}});
+      if (spill && (chunks.empty() || used + need > cap)) {
+        chunks.push_back(
+            {(int32_t)ki.size(), (int32_t)ki.size(), (int32_t)gi.size(), (int32_t)gi.size(), 0});
+        used = 0;
+      }
+      const int32_t span = (int32_t)(hd * k_tiles + k_base);
+      for (int32_t t = 0; t < nk; ++t) {
+        ki.push_back(BwdItem{(int32_t)b, hd, t, (int32_t)(hd * tiles + q_base), kr[t].lo, kr[t].hi,
+                             kr[t].full_lo, kr[t].full_hi, span + t, {0, 0, 0}});
+        spans[span + t] = KeySpan{(int32_t)(has_mask ? used : used - kr[t].lo), kr[t].lo, kr[t].hi, 0};
+        used += has_mask ? nq : kr[t].hi - kr[t].lo;
+      }
+      for (int32_t t = 0; spill && t < nq; t += 2) {
+        TileRange r = qr[t];
+        if (t + 1 < nq && qr[t + 1].hi > qr[t + 1].lo) {
+          r.lo = r.hi > r.lo ? std::min(r.lo, qr[t + 1].lo) : qr[t + 1].lo;
+          r.hi = std::max(r.hi, qr[t + 1].hi);
+        }
+        gi.push_back(BwdItem{(int32_t)b, hd, t / 2, 0, r.lo, r.hi, 0, 0, span, {0, 0, 0}});
+      }
+      if (spill) {
+        chunks.back().k1 = (int32_t)ki.size();
+        chunks.back().g1 = (int32_t)gi.size();
+        chunks.back().tiles = used;
+      }
+    }
+    q_base += nq;
+    k_base += nk;
   }
-  order_items(&qi, claims_items((int64_t)qi.size(), h->num_sms));
-  order_items(&ki, claims_items((int64_t)ki.size(), h->num_sms));
+  if (!spill) {
+    chunks.clear();
+    gi.clear();
+  }
+  order_items(qi.begin(), qi.end(), h->num_sms);
+  if (!spill) order_items(ki.begin(), ki.end(), h->num_sms);
+  for (const BwdState::Chunk& c : chunks) {
+    order_items(ki.begin() + c.k0, ki.begin() + c.k1, h->num_sms);
+    order_items(gi.begin() + c.g0, gi.begin() + c.g1, h->num_sms);
+  }
   const size_t seq_bytes = align_up(recs.size() * sizeof(SeqRec), 256);
   const size_t q_bytes = align_up(qi.size() * sizeof(BwdItem), 256);
-  const size_t total = seq_bytes + q_bytes + ki.size() * sizeof(BwdItem);
+  const size_t k_bytes = align_up(ki.size() * sizeof(BwdItem), 256);
+  const size_t g_bytes = align_up(gi.size() * sizeof(BwdItem), 256);
+  const size_t total = seq_bytes + q_bytes + k_bytes + g_bytes + spans.size() * sizeof(KeySpan);
   bw.valid = false;
   fa_status_t st = ensure_buffer(h, &bw.lists, total);
   if (st != FA_OK) return st;
   bw.host.assign(total, 0);
-  std::memcpy(bw.host.data(), recs.data(), recs.size() * sizeof(SeqRec));
-  if (!qi.empty()) std::memcpy(bw.host.data() + seq_bytes, qi.data(), qi.size() * sizeof(BwdItem));
-  if (!ki.empty())
-    std::memcpy(bw.host.data() + seq_bytes + q_bytes, ki.data(), ki.size() * sizeof(BwdItem));
+  uint8_t* at = bw.host.data();
+  auto put = [&](const void* src, size_t bytes, size_t room) {
+    if (bytes) std::memcpy(at, src, bytes);
+    at += room;
+  };
+  put(recs.data(), recs.size() * sizeof(SeqRec), seq_bytes);
+  put(qi.data(), qi.size() * sizeof(BwdItem), q_bytes);
+  put(ki.data(), ki.size() * sizeof(BwdItem), k_bytes);
+  put(gi.data(), gi.size() * sizeof(BwdItem), g_bytes);
+  put(spans.data(), spans.size() * sizeof(KeySpan), 0);
   // Pageable memory: the call returns once the source has been read.
   const cudaError_t e =
       cudaMemcpyAsync(bw.lists.ptr, bw.host.data(), total, cudaMemcpyHostToDevice, stream);
@@ -177,7 +241,10 @@ fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* c
   bw.valid = true;
   bw.n_q = (int32_t)qi.size();
   bw.n_k = (int32_t)ki.size();
+  bw.n_g = (int32_t)gi.size();
   bw.tiles = (int32_t)tiles;
+  bw.k_tiles = (int32_t)k_tiles;
+  bw.chunks.swap(chunks);
   bw.geo0 = recs.empty() ? SeqRec{} : recs[0];
   return FA_OK;
 }
@@ -226,13 +293,22 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   }
   st = refresh_lists(h, a.prefix, a.cu_q, a.cu_kv, has_mask, stream);
   if (st != FA_OK) return st;
+  int64_t ds_tiles = 0;
+  for (const BwdState::Chunk& c : h->bwd.chunks) ds_tiles = std::max(ds_tiles, c.tiles);
+  if (ds_tiles > 0 && ensure_buffer(h, &h->bwd.spill, (size_t)ds_tiles * 128 * 128 * 2) != FA_OK) {
+    clear_error();  // no room for dS: the walks that need none
+    h->bwd.no_spill = true;
+    st = refresh_lists(h, a.prefix, a.cu_q, a.cu_kv, has_mask, stream);
+    if (st != FA_OK) return st;
+    ds_tiles = 0;
+  }
   const BwdState& bw = h->bwd;
 
   // Scratch: row statistics | bias sums by tile and by distance, counters | the
   // dense mask's ranges and classes.
   const size_t stat_bytes = align_up((size_t)bw.tiles * d->N * 256 * sizeof(float), 256);
   const size_t W = a.bias ? (size_t)rel_width(a.bias->reach) : 0;
-  const size_t part_bytes = align_up((size_t)bw.tiles * d->N * W * sizeof(float), 256);
+  const size_t part_bytes = align_up((size_t)bw.k_tiles * d->N * W * sizeof(float), 256);
   const size_t dist_bytes = align_up((size_t)d->N * W * sizeof(double), 256);
   const int64_t planes = mask_planes(d, has_mask);
   const size_t occ_bytes = planes ? occupancy_bytes(planes, d->Sq, d->Skv) : 0;
@@ -247,11 +323,19 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   BwdParams p;
   std::memset(&p, 0, sizeof(p));
   p.seqs = reinterpret_cast<const SeqRec*>(lists);
-  BwdItem* q_items = reinterpret_cast<BwdItem*>(lists + seq_bytes);
-  BwdItem* k_items = reinterpret_cast<BwdItem*>(
-      lists + seq_bytes + align_up((size_t)bw.n_q * sizeof(BwdItem), 256));
+  uint8_t* at = lists + seq_bytes;
+  auto take = [&](int32_t n) {
+    BwdItem* items = reinterpret_cast<BwdItem*>(at);
+    at += align_up((size_t)n * sizeof(BwdItem), 256);
+    return items;
+  };
+  BwdItem* q_items = take(bw.n_q);
+  BwdItem* k_items = take(bw.n_k);
+  BwdItem* g_items = take(bw.n_g);
+  KeySpan* spans = reinterpret_cast<KeySpan*>(at);
   p.q_items = q_items;
   p.k_items = k_items;
+  p.spans = spans;
   p.n_q = bw.n_q;
   p.n_k = bw.n_k;
   p.stats = reinterpret_cast<float*>(scratch);
@@ -319,10 +403,13 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
       r.cls = oc.cls;
       r.q_items = q_items;
       r.k_items = k_items;
+      r.g_items = g_items;
+      r.spans = spans;
       r.occ_sb = d->mask_kind == FA_MASK_SS ? 0 : (d->mask_kind == FA_MASK_B1SS ? 1 : d->N);
       r.occ_sh = d->mask_kind == FA_MASK_BNSS ? 1 : 0;
       r.n_q = bw.n_q;
       r.n_k = bw.n_k;
+      r.n_g = bw.n_g;
       r.n_qt = oc.n_qt;
       r.n_kt = oc.n_kt;
       e = launch_bwd_ranges(r, stream);
@@ -332,7 +419,19 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   e = launch_bwd_stats((int)d->D, p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "row statistics launch");
   const char* why = nullptr;
-  e = launch_bwd((int)d->D, p, h->num_sms, stream, &why);
+  if (ds_tiles > 0) {
+    p.ds = static_cast<__nv_bfloat16*>(bw.spill.ptr);
+    for (size_t c = 0; c < bw.chunks.size() && e == cudaSuccess; ++c) {
+      const BwdState::Chunk& ch = bw.chunks[c];
+      p.k_items = k_items + ch.k0;
+      p.n_k = ch.k1 - ch.k0;
+      p.g_items = g_items + ch.g0;
+      p.n_g = ch.g1 - ch.g0;
+      e = launch_bwd((int)d->D, p, h->num_sms, stream, &why);
+    }
+  } else {
+    e = launch_bwd((int)d->D, p, h->num_sms, stream, &why);
+  }
   if (e != cudaSuccess) {
     if (why) return fail(FA_ERR_UNSUPPORTED, "launch refused: %s", why);
     return cuda_fail(e, "backward launch");
@@ -340,7 +439,7 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   if (a.bias) {
     if (bw.n_q > 0)
       e = launch_rel_reduce(p.rel_part, reinterpret_cast<double*>(scratch + stat_bytes + part_bytes),
-                            p.rel_done, p.rel_table.bucket_of, a.dtable, (int32_t)d->N, bw.tiles,
+                            p.rel_done, p.rel_table.bucket_of, a.dtable, (int32_t)d->N, bw.k_tiles,
                             a.bias->num_buckets, a.bias->reach, stream);
     else
       e = cudaMemsetAsync(a.dtable, 0, (size_t)a.bias->num_buckets * d->N * sizeof(float), stream);

@@ -93,14 +93,27 @@ __global__ void __launch_bounds__(256) bwd_stats(const __grid_constant__ BwdPara
   }
 }
 
-// Dense masks: thread n < n_q copies query item n's range, the warps after
-// them reduce one key item each: [lo, hi) from the first to the last query
+// Dense masks: thread n < n_q copies query item n's range, the n_g threads
+// after them join those of a dQ item, the warps after them reduce one key item each: [lo, hi) from the first to the last query
 // tile with a visible pair, and the longest run of fully visible ones (the
 // first on ties). A FULL class covers 128 stored keys.
 __global__ void __launch_bounds__(256) bwd_ranges(BwdOccParams a, int q_blocks) {
   if ((int)blockIdx.x < q_blocks) {
     const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.n_q) return;
+    if (n >= a.n_q) {
+      const int m = n - a.n_q;
+      if (m >= a.n_g) return;
+      BwdItem it = a.g_items[m];
+      const TileRange* r = a.ranges + (it.b * a.occ_sb + it.h * a.occ_sh) * a.n_qt + it.tile * 2;
+      it.lo = it.hi = 0;
+      for (int x = 0; x < 2 && it.tile * 2 + x < a.n_qt; ++x) {
+        if (r[x].hi <= r[x].lo) continue;
+        it.lo = it.hi > 0 ? min(it.lo, r[x].lo) : r[x].lo;
+        it.hi = max(it.hi, r[x].hi);
+      }
+      a.g_items[m] = it;
+      return;
+    }
     BwdItem it = a.q_items[n];
     const TileRange r = a.ranges[(it.b * a.occ_sb + it.h * a.occ_sh) * a.n_qt + it.tile];
     it.lo = r.lo, it.hi = r.hi, it.full_lo = r.full_lo, it.full_hi = r.full_hi;
@@ -137,9 +150,11 @@ __global__ void __launch_bounds__(256) bwd_ranges(BwdOccParams a, int q_blocks) 
   it.full_lo = best > 0 ? best_at : it.lo;
   it.full_hi = best > 0 ? best_at + best : it.lo;
   a.k_items[n] = it;
+  a.spans[it.span].lo = it.lo;
+  a.spans[it.span].hi = it.hi;
 }
 
-// dist[h][e] = sum over head h's query tiles, in 64 bits: one CTA per head and
+// dist[h][e] = sum over head h's key tiles, in 64 bits: one CTA per head and
 // 32 distances, warp w adds tiles w, w + 8, ... and the eight sums are added
 // in warp order. The last CTA of a head to finish then sums the distances of
 // each bucket, those past the reach with the end they clip to: one warp per
@@ -201,7 +216,7 @@ cudaError_t launch_bwd_stats(int D, const BwdParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_bwd_ranges(const BwdOccParams& a, cudaStream_t stream) {
-  const int qb = (a.n_q + 255) / 256, kb = (a.n_k + 7) / 8;
+  const int qb = (a.n_q + a.n_g + 255) / 256, kb = (a.n_k + 7) / 8;
   if (qb + kb > 0) bwd_ranges<<<qb + kb, 256, 0, stream>>>(a, qb);
   return cudaGetLastError();
 }

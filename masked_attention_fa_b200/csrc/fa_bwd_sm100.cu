@@ -49,15 +49,29 @@
 namespace fa {
 namespace dev {
 
-constexpr int kBwdThreads = 512;
-// Register split over the 512 x 128 registers of the launch.
-constexpr int kBwdRegsMath = 168, kBwdRegsEpi = 112, kBwdRegsControl = 64;
-static_assert(256 * kBwdRegsMath + 128 * kBwdRegsEpi + 128 * kBwdRegsControl == kBwdThreads * 128,
+// The 128 columns of a tile are shared out over groups of four math warps.
+// Four groups against two: more warps hide each other's latencies where the
+// math bounds a step (head dim 64: 658 -> 638 us on the bias backward of
+// 2 x 16 x 4096 x 64; at 128 the same within 1 %).
+constexpr int kGroups = 4, kCols = 128 / kGroups, kMathWarps = 4 * kGroups;
+constexpr int kWarpEpi = kMathWarps, kWarpMma = kWarpEpi + 4, kWarpLoad = kWarpMma + 1,
+              kWarpSums = kWarpMma + 3;
+constexpr int kBwdThreads = 32 * (kMathWarps + 8);
+// Register split over the registers of the launch.
+constexpr int kBwdRegsLaunch = 65536 / kBwdThreads / 8 * 8;
+constexpr int kBwdRegsMath = 88, kBwdRegsEpi = 72, kBwdRegsControl = 56;
+static_assert(32 * kMathWarps * kBwdRegsMath + 128 * kBwdRegsEpi + 128 * kBwdRegsControl ==
+                  kBwdThreads * kBwdRegsLaunch,
               "register split must equal the launch allocation");
+constexpr int kSumRow = kCols + 32;  // bias gradient: diagonals of 32 rows x kCols columns
 constexpr int kBwdBiasNone = 0, kBwdBiasAlibi = 1, kBwdBiasRel = 2;
 constexpr float kLog2e = 1.4426950408889634f;
-// Of 8 pairs of columns, how many take the FMA-pipe exponential.
-constexpr int kPolyOf8 = 3;
+// Of 8 pairs of columns, how many take the FMA-pipe exponential. At head dim
+// 64 the exponentials bound a step (0: 638, 2: 630, 4: 663 us on the bias
+// backward of 2 x 16 x 4096 x 64); at 128 the power cap does, and the MUFU unit
+// needs less (0: 457, 3: 463 us on a causal 2 x 16 x 4096 x 128).
+template <int D>
+constexpr int kPolyOf8 = D == 64 ? 2 : 0;
 
 // Where a wait gave up (error word bits 8..15), after the forward's sites.
 enum BwdSite : uint32_t {
@@ -67,19 +81,21 @@ enum BwdSite : uint32_t {
   kBSiteSumEmpty, kBSiteFarFull, kBSiteFarEmpty, kBSiteDrain, kBSiteSmem,
 };
 
-template <int D, bool kKeys>
+template <int D, bool kKeys, bool kRel>
 struct BCfg {
+  // The key walk sums the bias's gradient.
+  static constexpr bool kSums = kKeys && kRel;
   static constexpr int kChunks = D / 64;
   static constexpr uint32_t kChunkBytes = 128u * 128u;
   static constexpr uint32_t kTileBytes = 128u * D * 2u;
   // Ring depths. B0(t) is read first by S(t) and last by acc0(t), a step
   // later; B1(t) by dP(t) (and acc1(t)).
-  static constexpr int kN0 = (D == 128 && kKeys) ? 3 : 4;
+  static constexpr int kN0 = D == 64 || !kKeys ? 4 : (kSums ? 2 : 3);
   static constexpr int kN1 = D == 128 ? 2 : 4;
   static constexpr uint32_t kABytes = kKeys ? 2u * kTileBytes : 0u;
   static constexpr uint32_t kRingBytes = (kN0 + kN1) * kTileBytes;
   static constexpr uint32_t kStatBytes = kKeys ? 2u * 1024u : 0u;
-  static constexpr uint32_t kSumBytes = kKeys ? 0u : 2u * 8u * 96u * 4u;
+  static constexpr uint32_t kSumBytes = kSums ? 2u * kMathWarps * kSumRow * 4u : 0u;
   static constexpr uint32_t kCtlBytes = 1024u;
   static constexpr uint32_t kSmemBytes = kABytes + kRingBytes + kStatBytes + kSumBytes + kCtlBytes;
   static_assert(kSmemBytes <= 227u * 1024u, "shared memory budget");
@@ -104,7 +120,7 @@ struct BCtl {
   uint64_t drain;
   uint32_t tmem_base;
   volatile int abort_flag;
-  float far[8][2];
+  float far[kMathWarps][2];
 };
 static_assert(sizeof(BCtl) <= 1024, "barrier area");
 
@@ -169,18 +185,21 @@ __device__ __forceinline__ int bwd_item(int k) {
   return k * G + ((k & 1) ? (G - 1 - c) : c);
 }
 
-// The CTA's steps in order: tile t of an item that has tiles.
+// The CTA's steps in order: tile t of an item that has tiles. The query walk
+// goes up its key tiles, the key walk down its query tiles: distances grow
+// along both.
 struct Step {
   int k;        // next position of the CTA's list
   int t, lo, hi;
   bool valid, first, last;
 };
 
+template <bool kKeys>
 __device__ __forceinline__ void next_step(const BwdItem* items, int n, Step& s) {
-  if (s.valid && s.t + 1 < s.hi) {
-    ++s.t;
+  if (s.valid && !s.last) {
+    s.t += kKeys ? -1 : 1;
     s.first = false;
-    s.last = s.t + 1 == s.hi;
+    s.last = kKeys ? s.t == s.lo : s.t + 1 == s.hi;
     return;
   }
   for (;;) {
@@ -192,10 +211,11 @@ __device__ __forceinline__ void next_step(const BwdItem* items, int n, Step& s) 
     ++s.k;
     const int4 r = __ldg(reinterpret_cast<const int4*>(items + idx) + 1);  // lo, hi, full range
     if (r.y <= r.x) continue;
-    s.t = s.lo = r.x;
+    s.lo = r.x;
     s.hi = r.y;
+    s.t = kKeys ? s.hi - 1 : s.lo;
     s.valid = s.first = true;
-    s.last = s.t + 1 == s.hi;
+    s.last = s.lo + 1 == s.hi;
     return;
   }
 }
@@ -205,10 +225,10 @@ __device__ __forceinline__ void next_step(const BwdItem* items, int n, Step& s) 
 // TMA loads (a whole warp; lane 0 issues): per step the tile of B0, the row
 // statistics (key walk) and the tile of B1; in the key walk the item's K and
 // V follow its first tiles, as soon as the previous item has read its own.
-template <int D, bool kKeys>
+template <int D, bool kKeys, bool kRel>
 __device__ void bwd_load(const BwdParams& p, BCtl* ctl, uint8_t* sA, uint8_t* sB0, uint8_t* sB1,
                          uint8_t* sStat, const WaitCtx& w) {
-  using C = BCfg<D, kKeys>;
+  using C = BCfg<D, kKeys, kRel>;
   const int lane = threadIdx.x & 31;
   const BwdItem* items = kKeys ? p.k_items : p.q_items;
   const int n_items = kKeys ? p.n_k : p.n_q;
@@ -259,11 +279,12 @@ __device__ void bwd_load(const BwdParams& p, BCtl* ctl, uint8_t* sA, uint8_t* sB
     const SeqRec sr = p.seqs[it.b];
     const int bc = p.tnd ? 0 : it.b;
     const int off = kKeys ? sr.q_off : sr.kv_off, len = kKeys ? sr.sq : sr.skv;
-    for (int t = it.lo; t < it.hi && ok; ++t) {
+    for (int x = 0; x < it.hi - it.lo && ok; ++x) {
+      const int t = kKeys ? it.hi - 1 - x : it.lo + x;
       const int row = off + t * 128, rows = min(128, len - t * 128);
       ok = load_b(sB0, ctl->b0_full, ctl->b0_empty, n0, C::kN0, tm0, row, rows, it.h, bc,
                   kBSiteB0Empty);
-      if (kKeys && ok && t == it.lo) {
+      if (kKeys && ok && x == 0) {
         ok = na0 == 0 || wait_warp(&ctl->a0_empty, (na0 - 1) & 1u, w, kBSiteA0Empty);
         if (ok && lane == 0)
           tma_tile(sA, &p.tm_k, &ctl->a0_full, sr.kv_off + it.tile * 128, it.h, bc);
@@ -282,7 +303,7 @@ __device__ void bwd_load(const BwdParams& p, BCtl* ctl, uint8_t* sA, uint8_t* sB
       if (ok)
         ok = load_b(sB1, ctl->b1_full, ctl->b1_empty, n1, C::kN1, tm1, row, rows, it.h, bc,
                     kBSiteB1Empty);
-      if (kKeys && ok && t == it.lo) {
+      if (kKeys && ok && x == 0) {
         ok = na1 == 0 || wait_warp(&ctl->a1_empty, (na1 - 1) & 1u, w, kBSiteA1Empty);
         if (ok && lane == 0)
           tma_tile(sA + C::kTileBytes, &p.tm_v, &ctl->a1_full, sr.kv_off + it.tile * 128, it.h, bc);
@@ -305,6 +326,12 @@ __device__ void bwd_load(const BwdParams& p, BCtl* ctl, uint8_t* sA, uint8_t* sB
   __syncwarp();
 }
 
+// Descriptor of an MN-major operand without swizzle: 8 x 16-byte core matrices,
+// groups of 8 K rows lbo apart, blocks of 8 MN elements sbo apart.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return sdesc(addr, lbo, sbo) & ~(7ull << 61);
+}
+
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -318,9 +345,9 @@ __device__ __forceinline__ bool elect_one() {
 
 // D[128 x 128] = A B^T, both K-major over the head dim; A in shared memory
 // (key walk) or tensor memory.
-template <int D, bool kKeys>
+template <int D, bool kKeys, bool kRel>
 __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a_tmem, uint64_t a0, uint64_t b0) {
-  using C = BCfg<D, kKeys>;
+  using C = BCfg<D, kKeys, kRel>;
   constexpr uint32_t idesc = idesc_bf16(128, 128, false);
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) {
@@ -331,17 +358,18 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a_tmem, uint64
 }
 
 // acc[128 x D] += W B over half of W's columns, W (P or dS, bf16) in tensor
-// memory: columns 0..63 in the first 32 tensor memory columns from `a`,
-// 64..127 from a + 64. Half 0 takes the columns 0..31 and 64..95 (what each
-// math warp stores first), half 1 the others.
-template <int D, bool kKeys>
+// memory: columns kCols * g and on from tensor memory column a + kCols * g.
+// Half 0 takes the first half of every group's columns (what each math warp
+// stores first), half 1 the others.
+template <int D>
 __device__ __forceinline__ void issue_acc(uint32_t d, uint32_t a, uint64_t b0, uint32_t accumulate,
                                           int half) {
   constexpr uint32_t idesc = idesc_bf16(128, D, true);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int k = (q >> 1) * 4 + half * 2 + (q & 1);  // 16 columns of W, 16 rows of B
-    mma_ts(d, a + (k >> 2) * 64u + (k & 3) * 8u, b0 + (uint64_t)(k * (2048u >> 4)), idesc,
+    constexpr int kRun = kCols / 32;  // 16-column steps of a group's half
+    const int k = (q / kRun) * (2 * kRun) + half * kRun + q % kRun;  // 16 columns of W, 16 rows of B
+    mma_ts(d, a + (16 * k / kCols) * kCols + (16 * k % kCols) / 2, b0 + (uint64_t)(k * (2048u >> 4)), idesc,
            q > 0 ? 1u : accumulate);
   }
 }
@@ -350,10 +378,10 @@ __device__ __forceinline__ void issue_acc(uint32_t d, uint32_t a, uint64_t b0, u
 // uniform registers; one lane issues). The products that overwrite tensor
 // memory which an earlier product still reads are issued after it by this
 // same thread: products execute in order.
-template <int D, bool kKeys>
+template <int D, bool kKeys, bool kRel>
 __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint8_t* sA,
                         const uint8_t* sB0, const uint8_t* sB1, const WaitCtx& w) {
-  using C = BCfg<D, kKeys>;
+  using C = BCfg<D, kKeys, kRel>;
   const BwdItem* items = kKeys ? p.k_items : p.q_items;
   const int n_items = kKeys ? p.n_k : p.n_q;
   const uint32_t tS = tmem + C::kColS, tDP = tmem + C::kColDP;
@@ -368,7 +396,7 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
   Step cur, nx;
   nx.k = 0;
   nx.valid = false;
-  next_step(items, n_items, nx);
+  next_step<kKeys>(items, n_items, nx);
   uint32_t n = 0;       // step of nx
   uint32_t a0 = 0, a1 = 0;  // held operands awaited
   uint32_t items_done = 0;
@@ -385,7 +413,7 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
   };
   auto scores = [&]() {
     if (elect_one()) {
-      issue_scores<D, kKeys>(tS, tmem + C::kColA0, dA0, dB0 + (n % C::kN0) * kSlot);
+      issue_scores<D, kKeys, kRel>(tS, tmem + C::kColA0, dA0, dB0 + (n % C::kN0) * kSlot);
       mma_commit(&ctl->s_full);
       if (nx.last) mma_commit(&ctl->a0_empty);
     }
@@ -393,7 +421,7 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
   };
   auto dprobs = [&]() {
     if (elect_one()) {
-      issue_scores<D, kKeys>(tDP, tmem + C::kColA1, dA1, dB1 + (n % C::kN1) * kSlot);
+      issue_scores<D, kKeys, kRel>(tDP, tmem + C::kColA1, dA1, dB1 + (n % C::kN1) * kSlot);
       mma_commit(&ctl->dp_full);
       if (!kKeys) mma_commit(&ctl->b1_empty[n % C::kN1]);
       if (nx.last) mma_commit(&ctl->a1_empty);
@@ -409,7 +437,7 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
   while (ok && nx.valid) {
     cur = nx;
     const uint32_t c = n;
-    next_step(items, n_items, nx);
+    next_step<kKeys>(items, n_items, nx);
     ++n;
     if (nx.valid && !operands0()) break;
     if constexpr (kKeys) {
@@ -427,7 +455,7 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
         }
         tc_fence_after();
         if (elect_one()) {
-          issue_acc<D, kKeys>(tmem + C::kColAcc1, tS, dM1 + st * kSlot,
+          issue_acc<D>(tmem + C::kColAcc1, tS, dM1 + st * kSlot,
                               (cur.first && half == 0) ? 0u : 1u, half);
           if (half) {
             mma_commit(&ctl->b1_empty[st]);
@@ -451,8 +479,8 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
     tc_fence_after();
     const uint32_t st = c % C::kN0;
     if (elect_one()) {
-      issue_acc<D, kKeys>(tmem + C::kColAcc0, tDP, dM0 + st * kSlot, cur.first ? 0u : 1u, 0);
-      issue_acc<D, kKeys>(tmem + C::kColAcc0, tDP, dM0 + st * kSlot, 1u, 1);
+      issue_acc<D>(tmem + C::kColAcc0, tDP, dM0 + st * kSlot, cur.first ? 0u : 1u, 0);
+      issue_acc<D>(tmem + C::kColAcc0, tDP, dM0 + st * kSlot, 1u, 1);
       mma_commit(&ctl->b0_empty[st]);
       if (cur.last) mma_commit(&ctl->acc_full[0]);
     }
@@ -467,10 +495,16 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
   wait_bounded(&ctl->drain, 0u, w, kBSiteDrain, false);
 }
 
-// One bit per column of [0, 64): inside [lo, hi].
-__device__ __forceinline__ void interval_bits(int lo, int hi, uint32_t (&wm)[2]) {
+__device__ __forceinline__ void tmem_ld_wait(uint32_t a, uint32_t (&r)[32]) { tmem_ld32_wait(a, r); }
+__device__ __forceinline__ void tmem_ld_wait(uint32_t a, uint32_t (&r)[64]) { tmem_ld64_wait(a, r); }
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[8]) { tmem_st8(a, r); }
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[16]) { tmem_st16(a, r); }
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[32]) { tmem_st32(a, r); }
+
+// One bit per column of [0, kCols): inside [lo, hi].
+__device__ __forceinline__ void interval_bits(int lo, int hi, uint32_t (&wm)[kCols / 32]) {
 #pragma unroll
-  for (int wd = 0; wd < 2; ++wd) {
+  for (int wd = 0; wd < kCols / 32; ++wd) {
     const int a = lo - 32 * wd, b = hi - 32 * wd;
     const uint32_t upto = b >= 31 ? 0xffffffffu : (b < 0 ? 0u : (0xffffffffu >> (31 - b)));
     const uint32_t from = a <= 0 ? 0xffffffffu : (a > 31 ? 0u : (0xffffffffu << a));
@@ -478,23 +512,24 @@ __device__ __forceinline__ void interval_bits(int lo, int hi, uint32_t (&wm)[2])
   }
 }
 
-// P and dS of one half (64 columns) of every tile, one row per thread. Per
+// P and dS of one group's columns of every tile, one row per thread. Per
 // step: S to registers, P = 2^(scale log2e S + bias - lse log2e) (masked
 // entries 0), in the key walk P back in bf16 over S; then dP to registers,
 // dS = P (dP - delta) back in bf16 over dP. P is rounded to bf16 only as an
-// operand of dV; dS uses the fp32 value.
+// operand of dV; dS uses the fp32 value. With p.ds the key walk also writes
+// dS in bf16 to global memory, for the dQ kernel.
 template <int D, bool kKeys, int kBias>
 __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint8_t* sStat,
                          float* sSum, const WaitCtx& w) {
-  using C = BCfg<D, kKeys>;
   constexpr bool kRel = kBias == kBwdBiasRel;
-  constexpr bool kGrad = kRel && !kKeys;
+  using C = BCfg<D, kKeys, kRel>;
+  constexpr bool kGrad = C::kSums;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wq = warp & 3, g = warp >> 2;
   const int row = wq * 32 + lane;
   const uint32_t lane_bits = (uint32_t)(wq * 32) << 16;
-  const uint32_t tS = tmem + lane_bits + C::kColS + 64u * g;
-  const uint32_t tDP = tmem + lane_bits + C::kColDP + 64u * g;
+  const uint32_t tS = tmem + lane_bits + C::kColS + kCols * g;
+  const uint32_t tDP = tmem + lane_bits + C::kColDP + kCols * g;
   const BwdItem* items = kKeys ? p.k_items : p.q_items;
   const int n_items = kKeys ? p.n_k : p.n_q;
   const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
@@ -538,19 +573,29 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
     if constexpr (kRel) ext = p.rel.ext + (int64_t)it.h * 4 * p.rel.row;
     float far_lo = 0.f, far_hi = 0.f;
 
-    for (int t = it.lo; t < it.hi; ++t, ++n) {
+    // Spilled dS: this thread's first 8 columns in the item's tile t = 0.
+    __nv_bfloat16* ds_out = nullptr;
+    bool ragged = false;
+    if (kKeys && p.ds) {
+      ds_out = p.ds + (int64_t)p.spans[it.span].first * (128 * 128) + g * (kCols * 128) + row * 8;
+      ragged = (it.tile + 1) * 128 > sr.skv;
+    }
+    for (int s = 0; s < it.hi - it.lo; ++s, ++n) {
+      const int t = kKeys ? it.hi - 1 - s : it.lo + s;
       const bool partial = !(t >= it.full_lo && t < it.full_hi);
-      const int c0 = t * 128 + 64 * g;  // first column of this half
+      const int c0 = t * 128 + kCols * g;  // first column of this half
       // Distance key - diagonal of the row's column 0; it grows with the
       // column in the query walk and falls with it in the key walk.
       const int rel0 = kKeys ? at - (c0 + delta) : c0 - (at + delta);
-      uint32_t wm[2] = {0xffffffffu, 0xffffffffu};
+      uint32_t wm[kCols / 32];
+#pragma unroll
+      for (int wd = 0; wd < kCols / 32; ++wd) wm[wd] = 0xffffffffu;
       if (partial) {
         interval_bits(v_lo - c0, v_hi - c0, wm);
         if (mrow != nullptr) {
           const uint8_t* mt = mrow + c0 * m_step;
 #pragma unroll
-          for (int wd = 0; wd < 2; ++wd) {
+          for (int wd = 0; wd < kCols / 32; ++wd) {
             uint32_t see = wm[wd], hide = 0u;
 #pragma unroll 8
             for (int c = 0; c < 32; ++c)
@@ -559,7 +604,7 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
           }
         }
       }
-      const float* st = reinterpret_cast<const float*>(sStat + (n & 1u) * 1024u) + 64 * g;
+      const float* st = reinterpret_cast<const float*>(sStat + (n & 1u) * 1024u) + kCols * g;
       if (kKeys && !wait_warp(&ctl->stat_full[n & 1u], (n >> 1) & 1u, w, kBSiteStatFull)) {
         ok = false;
         break;
@@ -569,12 +614,12 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
         break;
       }
       tc_fence_after();
-      float x[64];
+      float x[kCols];
       {
-        uint32_t sv[64];
-        tmem_ld64_wait(tS, sv);
+        uint32_t sv[kCols];
+        tmem_ld_wait(tS, sv);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(sv[c]);
+        for (int c = 0; c < kCols; ++c) x[c] = __uint_as_float(sv[c]);
       }
       if constexpr (!kKeys) {
         tc_fence_before();
@@ -596,7 +641,7 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
         const float d0 = (float)rel0;
         constexpr float kSign = kKeys ? -1.f : 1.f;
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
+        for (int c = 0; c < kCols; c += 2) {
           float da = d0, db = d0;
           add_x2(da, db, kSign * c, kSign * (c + 1));
           if (p.alibi == FA_ALIBI_SQRT) {
@@ -618,7 +663,7 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
         const float4* src =
             reinterpret_cast<const float4*>(ext + (int64_t)(first & 3) * p.rel.row + (first & ~3));
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
+        for (int c = 0; c < kCols; c += 4) {
           float4 e = __ldg(kKeys ? src - c / 4 : src + c / 4);
           if (kKeys) e = make_float4(e.w, e.z, e.y, e.x);
           if constexpr (kKeys) {
@@ -635,7 +680,7 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
       } else {
         const uint64_t l2 = pack_f32x2(nl + base, nl + base);
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
+        for (int c = 0; c < kCols; c += 4) {
           if constexpr (kKeys) {
             float4 l = *reinterpret_cast<const float4*>(st + c);
             if constexpr (kRel) {
@@ -652,14 +697,14 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
       }
       if (partial) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
+        for (int c = 0; c < kCols; ++c)
           x[c] = ((wm[c >> 5] >> (c & 31)) & 1u) ? x[c] : -INFINITY;
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int c = 32 * half; c < 32 * half + 32; c += 2) {
-          if (((c >> 1) * kPolyOf8) % 8 < kPolyOf8) {
+        for (int c = kCols / 2 * half; c < kCols / 2 * (half + 1); c += 2) {
+          if (((c >> 1) * kPolyOf8<D>) % 8 < kPolyOf8<D>) {
             ex2_floor_x2<kGrad ? 5 : 4>(x[c], x[c + 1]);
           } else {
             x[c] = ex2(x[c]);
@@ -667,11 +712,11 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
           }
         }
         if constexpr (kKeys) {
-          uint32_t pk[16];
+          uint32_t pk[kCols / 4];
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            pk[c] = pack_bf16(x[32 * half + 2 * c], x[32 * half + 2 * c + 1]);
-          tmem_st16(tS + 16u * half, pk);
+          for (int c = 0; c < kCols / 4; ++c)
+            pk[c] = pack_bf16(x[kCols / 2 * half + 2 * c], x[kCols / 2 * half + 2 * c + 1]);
+          tmem_st(tS + kCols / 4 * half, pk);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -684,10 +729,10 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
       }
       tc_fence_after();
       {
-        uint32_t dv[64];
-        tmem_ld64_wait(tDP, dv);
+        uint32_t dv[kCols];
+        tmem_ld_wait(tDP, dv);
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
+        for (int c = 0; c < kCols; c += 4) {
           float y[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) y[q] = __uint_as_float(dv[c + q]);
@@ -704,10 +749,10 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
         }
       }
       {
-        uint32_t pk[32];
+        uint32_t pk[kCols / 2];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
-        tmem_st32(tDP, pk);
+        for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
+        tmem_st(tDP, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -715,14 +760,29 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
           mbar_arrive(&ctl->ds_full);
           if (kKeys) mbar_arrive(&ctl->stat_empty[n & 1u]);
         }
+        if (kKeys && ds_out) {
+          // Rows past the sequence's end go out as zeros, dQ sums over them.
+          if (ragged && !stored) {
+#pragma unroll
+            for (int c = 0; c < kCols / 2; ++c) pk[c] = 0u;
+          }
+          // 8 columns of a warp's rows are 512 contiguous bytes. (Rows of the
+          // whole tile are 32 lines a store, which keep shared memory from the
+          // products: key walk 252 us against 234 on a causal 2 x 16 x 4096 x 128.)
+          __nv_bfloat16* dst = ds_out + (int64_t)t * (128 * 128);
+#pragma unroll
+          for (int u = 0; u < kCols / 8; ++u)
+            st_global_na_v4(dst + u * (8 * 128),
+                            make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]));
+        }
       }
       if constexpr (kGrad) {
         if (!stored) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = 0.f;
+          for (int c = 0; c < kCols; ++c) x[c] = 0.f;
         }
         if (near) {
-          // Sums by diagonal of this warp's 32 rows x 64 columns: the running
+          // Sums by diagonal of this warp's 32 rows x kCols columns: the running
           // sum of a diagonal moves to the next lane with each column, and
           // leaves at lane 31 (entry c) or after the last column.
           const uint32_t buf = n_near & 1u;
@@ -731,22 +791,22 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
             ok = false;
             break;
           }
-          float* out = sSum + (buf * 8 + warp) * 96;
+          float* out = sSum + (buf * kMathWarps + warp) * kSumRow;
           float s = 0.f;
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
+          for (int c = 0; c < kCols; ++c) {
             const float up = __shfl_up_sync(0xffffffffu, s, 1);
             s = (lane == 0 ? 0.f : up) + x[c];
             if (lane == 31) out[c] = s;
           }
-          if (lane < 31) out[94 - lane] = s;
+          if (lane < 31) out[kCols + 30 - lane] = s;
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->sum_full[buf]);
           ++n_near;
         } else {
           float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
+          for (int c = 0; c < kCols; c += 4) {
             add_x2(acc[0], acc[1], x[c], x[c + 1]);
             add_x2(acc[2], acc[3], x[c + 2], x[c + 3]);
           }
@@ -774,49 +834,51 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
   }
 }
 
-// Bias gradient (one warp, query walk): the item's sums by distance, entry e
-// for the distance e - reach - kRelPad, each written once. Diagonal d of a
-// tile (d = column - row + 127) gathers entry x = d - 96 - 64 g + 32 wq of
-// each math warp (g, wq); the diagonals 128..254 of a tile are 0..126 of the
-// next one and wait for it in registers. Entry 0 and the last take the tiles
-// past the reach, which near tiles cannot touch.
-template <int D>
+// Bias gradient (one warp, key walk): the item's sums by distance, entry e for
+// the distance e - reach - kRelPad, each written once. Diagonal y of a tile
+// (y = column - row + 127) gathers entry y - 96 - kCols g + 32 wq of each math
+// warp (g, wq). In the order of growing distance, d = 254 - y, the sums
+// d >= 128 of a step are d - 128 of the next one (the query tile before) and
+// wait for it in registers. Entry 0 and the last take the tiles past the
+// reach, which near tiles cannot touch.
 __device__ void bwd_sums(const BwdParams& p, BCtl* ctl, const float* sSum, const WaitCtx& w) {
   const int lane = threadIdx.x & 31;
   const int width = rel_width(p.rel.reach);
   uint32_t n_near = 0, n_far = 0;
   for (int k = 0;; ++k) {
     const int idx = bwd_item(k);
-    if (idx >= p.n_q) return;
-    const BwdItem it = p.q_items[idx];
-    float* out = p.rel_part + (int64_t)it.stat * width;
+    if (idx >= p.n_k) return;
+    const BwdItem it = p.k_items[idx];
+    float* out = p.rel_part + (int64_t)it.span * width;
     for (int e = lane; e < width; e += 32) out[e] = 0.f;
     __syncwarp();
     if (it.hi <= it.lo) continue;
     const SeqRec sr = p.seqs[it.b];
-    const int diag0 = -(it.tile * 128 + 127 + (sr.skv - sr.sq)) + p.rel.reach + kRelPad;
+    const int diag0 = p.rel.reach + kRelPad - 127 - (sr.skv - sr.sq);
     float carry[4] = {0.f, 0.f, 0.f, 0.f};
     int pending = -1;  // entry of carry[0] of lane 0
-    for (int t = it.lo; t < it.hi; ++t) {
-      const int top = t * 128 + 127 - (it.tile * 128 + (sr.skv - sr.sq));
+    for (int t = it.hi - 1; t >= it.lo; --t) {
+      const int off = it.tile - t;
+      const int top = off * 128 + 127 - (sr.skv - sr.sq);
       if (top <= -p.rel.reach || top - 254 >= p.rel.reach) continue;
       const uint32_t buf = n_near & 1u;
       if (!wait_warp(&ctl->sum_full[buf], (n_near >> 1) & 1u, w, kBSiteSumFull)) return;
-      const float* in = sSum + buf * 8 * 96;
+      const float* in = sSum + buf * kMathWarps * kSumRow;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int d = q * 32 + lane;
         float lo = carry[q], hi = 0.f;
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          const int x = d - (96 + 64 * (m >> 2) - 32 * (m & 3));
-          if (x >= 0 && x < 95) lo += in[m * 96 + x];
-          if (x + 128 >= 0 && x + 128 < 95) hi += in[m * 96 + x + 128];
+        for (int m = 0; m < kMathWarps; ++m) {
+          const int base = 96 + kCols * (m >> 2) - 32 * (m & 3);
+          const int x = 254 - d - base, y = 126 - d - base;
+          if (x >= 0 && x < kCols + 31) lo += in[m * kSumRow + x];
+          if (y >= 0 && y < kCols + 31) hi += in[m * kSumRow + y];
         }
-        out[diag0 + t * 128 + d] = lo;
+        out[diag0 + off * 128 + d] = lo;
         carry[q] = hi;
       }
-      pending = diag0 + (t + 1) * 128;
+      pending = diag0 + (off + 1) * 128;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->sum_empty[buf]);
       ++n_near;
@@ -831,7 +893,7 @@ __device__ void bwd_sums(const BwdParams& p, BCtl* ctl, const float* sSum, const
     if (lane < 2) {
       float s = 0.f;
 #pragma unroll
-      for (int m = 0; m < 8; ++m) s += ctl->far[m][lane];
+      for (int m = 0; m < kMathWarps; ++m) s += ctl->far[m][lane];
       out[lane ? width - 1 : 0] = s;
     }
     __syncwarp();
@@ -844,9 +906,9 @@ __device__ void bwd_sums(const BwdParams& p, BCtl* ctl, const float* sSum, const
 // query walk it also brings Q and dO of the next item into tensor memory, a
 // row per thread, once the last product of the current item that reads them
 // is done.
-template <int D, bool kKeys>
+template <int D, bool kKeys, bool kRel>
 __device__ void bwd_epilogue(const BwdParams& p, BCtl* ctl, uint32_t tmem, const WaitCtx& w) {
-  using C = BCfg<D, kKeys>;
+  using C = BCfg<D, kKeys, kRel>;
   const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int row = wq * 32 + lane;
   const uint32_t lane_bits = (uint32_t)(wq * 32) << 16;
@@ -897,10 +959,13 @@ __device__ void bwd_epilogue(const BwdParams& p, BCtl* ctl, uint32_t tmem, const
                        ((int64_t)(kKeys ? sr.kv_off : sr.q_off) + at) * st;
     const bool v8 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
     if (it.hi <= it.lo) {
-      if (stored)
-#pragma unroll 1
-        for (int x = 0; x < D / 8; ++x)
-          st_global_na_v4(reinterpret_cast<uint4*>(o) + x, make_uint4(0u, 0u, 0u, 0u));
+      // Zeros, whole rows per group of lanes.
+      constexpr int kLanes = D / 8;
+      const int rows = min(128, (kKeys ? sr.skv : sr.sq) - it.tile * 128);
+#pragma unroll 4
+      for (int r = wq * 32 + lane / kLanes; r < min(rows, wq * 32 + 32); r += 32 / kLanes)
+        st_global_na_v4(reinterpret_cast<uint4*>(o + (int64_t)(r - row) * st) + lane % kLanes,
+                        make_uint4(0u, 0u, 0u, 0u));
       return true;
     }
     if (!wait_warp(&ctl->acc_full[which], done & 1u, w, kBSiteAccFull)) return false;
@@ -962,7 +1027,8 @@ __device__ void bwd_epilogue(const BwdParams& p, BCtl* ctl, uint32_t tmem, const
 
 template <int D, bool kKeys, int kBias>
 __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_constant__ BwdParams p) {
-  using C = BCfg<D, kKeys>;
+  constexpr bool kRel = kBias == kBwdBiasRel;
+  using C = BCfg<D, kKeys, kRel>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sA = smem;
   uint8_t* sB0 = sA + C::kABytes;
@@ -984,11 +1050,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->stat_full[s], 1);
-      mbar_init(&ctl->stat_empty[s], 8);
-      mbar_init(&ctl->p_full[s], 8);
+      mbar_init(&ctl->stat_empty[s], kMathWarps);
+      mbar_init(&ctl->p_full[s], kMathWarps);
       mbar_init(&ctl->acc_full[s], 1);
       mbar_init(&ctl->acc_free[s], 4);
-      mbar_init(&ctl->sum_full[s], 8);
+      mbar_init(&ctl->sum_full[s], kMathWarps);
       mbar_init(&ctl->sum_empty[s], 1);
     }
     mbar_init(&ctl->fix, 1);
@@ -997,16 +1063,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
     mbar_init(&ctl->a0_empty, 1);
     mbar_init(&ctl->a1_empty, 1);
     mbar_init(&ctl->s_full, 1);
-    mbar_init(&ctl->s_free, 8);
+    mbar_init(&ctl->s_free, kMathWarps);
     mbar_init(&ctl->dp_full, 1);
-    mbar_init(&ctl->ds_full, 8);
-    mbar_init(&ctl->far_full, 8);
+    mbar_init(&ctl->ds_full, kMathWarps);
+    mbar_init(&ctl->far_full, kMathWarps);
     mbar_init(&ctl->far_empty, 1);
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) {
+  if (warp == kWarpMma) {
     asm volatile(
         "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
             smem_u32(&ctl->tmem_base)),
@@ -1018,102 +1084,398 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
-  if constexpr (!kKeys) {
-    // What is above ran beside the row statistics' kernel; what is below reads
-    // them. The two walks need nothing of each other: from here on the key
-    // walk may take each SM that is free.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  }
+  // What is above ran beside the launch ahead of this one; what is below reads
+  // its results, but for the key walk behind a query walk: the two need nothing
+  // of each other, and each SM that is free may start on it.
+  if (!kKeys || p.ds) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const WaitCtx w{&ctl->abort_flag, p.err_word, p.timeout_ns};
-  if (warp < 8) {
+  if (warp < kMathWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwdRegsMath));
     bwd_math<D, kKeys, kBias>(p, ctl, tmem, sStat, sSum, w);
-  } else if (warp < 12) {
+  } else if (warp < kWarpMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwdRegsEpi));
-    bwd_epilogue<D, kKeys>(p, ctl, tmem, w);
+    bwd_epilogue<D, kKeys, kRel>(p, ctl, tmem, w);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwdRegsControl));
-    if (warp == 12) bwd_mma<D, kKeys>(p, ctl, tmem, sA, sB0, sB1, w);
-    if (warp == 13) bwd_load<D, kKeys>(p, ctl, sA, sB0, sB1, sStat, w);
-    if constexpr (kBias == kBwdBiasRel && !kKeys)
-      if (warp == 15) bwd_sums<D>(p, ctl, sSum, w);
+    if (warp == kWarpMma) bwd_mma<D, kKeys, kRel>(p, ctl, tmem, sA, sB0, sB1, w);
+    if (warp == kWarpLoad) bwd_load<D, kKeys, kRel>(p, ctl, sA, sB0, sB1, sStat, w);
+    if constexpr (C::kSums)
+      if (warp == kWarpSums) bwd_sums(p, ctl, sSum, w);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) {
+  if (warp == kWarpMma) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(C::kTmemCols)
                  : "memory");
   }
   // The key walk may have started beside the query walk: it ends after it,
   // so that what follows in the stream follows both.
-  if constexpr (kKeys) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (kKeys && !p.ds) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ------------------------------------------------------------- dQ from dS
+// dQ of two query tiles per item from the dS that the key walk wrote: dQ += dS
+// K over the key tiles, dS^T [keys x queries] read MN-major as the A operand.
+// One pass over dS from memory (32 KB a tile against 512 cycles of products at
+// head dim 128) bounds it; two query tiles share each tile of K, which halves
+// what L2 delivers. A ring of 32 KB slots takes K, then the dS of the one or
+// two query tiles, of each key tile.
+//   warps 0-7 epilogue (four per query tile), 8 products, 9 loads
+constexpr int kDqThreads = 320, kDqSlots = 7;
+constexpr uint32_t kDqSlotBytes = 128u * 128u * 2u;
+
+template <int D>
+struct DCfg {
+  static constexpr uint32_t kKBytes = 128u * D * 2u;
+  static constexpr uint32_t kSmemBytes = kDqSlots * kDqSlotBytes + 1024u;
+  static constexpr uint32_t kTmemCols = 4 * D;  // two query tiles, two items
+};
+
+struct DCtl {
+  uint64_t full[kDqSlots], empty[kDqSlots], fix;
+  uint64_t acc_full[2], acc_free[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+};
+
+// Which of the item's two query tiles key tile n holds dS for (bits 0 and 1),
+// and the index of the first one's tile of dS.
+__device__ __forceinline__ int held_tiles(const BwdParams& p, const BwdItem& it, int n, int& at) {
+  const int4 s = __ldg(reinterpret_cast<const int4*>(p.spans + it.span + n));  // first, lo, hi
+  const int i = it.tile * 2;
+  at = s.x + i;
+  return (i >= s.y && i < s.z ? 1 : 0) | (i + 1 >= s.y && i + 1 < s.z ? 2 : 0);
+}
+
+template <int D>
+__device__ void dq_load(const BwdParams& p, DCtl* ctl, uint8_t* smem, const WaitCtx& w) {
+  using C = DCfg<D>;
+  const int lane = threadIdx.x & 31;
+  uint32_t n_slot = 0, nfix = 0;
+  bool ok = true, fixing = false;
+  auto slot_free = [&]() -> bool {
+    return n_slot < kDqSlots || wait_warp(&ctl->empty[n_slot % kDqSlots],
+                                          ((n_slot / kDqSlots) - 1) & 1u, w, kBSiteB0Empty);
+  };
+  for (int k = 0; ok; ++k) {
+    const int idx = bwd_item(k);
+    if (idx >= p.n_g) break;
+    const BwdItem it = p.g_items[idx];
+    const SeqRec sr = p.seqs[it.b];
+    for (int n = it.lo; n < it.hi && ok; ++n) {
+      int at;
+      const int held = held_tiles(p, it, n, at);
+      if (!held) continue;
+      if (!slot_free()) {
+        ok = false;
+        break;
+      }
+      uint32_t st = n_slot % kDqSlots;
+      uint8_t* dst = smem + st * kDqSlotBytes;
+      const int rows = min(128, sr.skv - n * 128);
+      const bool clear = p.tnd && rows < 128;  // K rows of the next packed sequence
+      if (lane == 0) {
+        uint64_t* bar = clear ? &ctl->fix : &ctl->full[st];
+        mbar_expect_tx(bar, C::kKBytes);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(dst + c * 16384, &p.tm_k, bar, c * 64, sr.kv_off + n * 128, it.h,
+                      p.tnd ? 0 : it.b);
+      }
+      __syncwarp();
+      if (clear) {
+        fixing = true;
+        if (!wait_warp(&ctl->fix, nfix & 1u, w, kBSiteFix)) {
+          ok = false;
+          break;
+        }
+        fixing = false;
+        ++nfix;
+        for (int x = rows * 8 + lane; x < 128 * 8; x += 32)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            st_shared_v4(smem_u32(dst) + c * 16384 + x * 16, 0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->full[st]);
+      }
+      ++n_slot;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (!ok || !((held >> q) & 1)) continue;
+        if (!slot_free()) {
+          ok = false;
+          continue;
+        }
+        st = n_slot % kDqSlots;
+        if (lane == 0) {
+          mbar_expect_tx(&ctl->full[st], kDqSlotBytes);
+          bulk_load(smem + st * kDqSlotBytes, p.ds + (int64_t)(at + q) * (128 * 128), kDqSlotBytes,
+                    &ctl->full[st]);
+        }
+        __syncwarp();
+        ++n_slot;
+      }
+    }
+  }
+  if (!ok && lane == 0) {
+    if (fixing) wait_bounded(&ctl->fix, nfix & 1u, w, kBSiteDrain, false);
+    for (uint32_t r = n_slot > kDqSlots ? n_slot - kDqSlots : 0u; r < n_slot; ++r)
+      wait_bounded(&ctl->full[r % kDqSlots], (r / kDqSlots) & 1u, w, kBSiteDrain, false);
+  }
+  __syncwarp();
+}
+
+template <int D>
+__device__ void dq_mma(const BwdParams& p, DCtl* ctl, uint32_t tmem, const uint8_t* smem,
+                       const WaitCtx& w) {
+  constexpr uint32_t idesc = idesc_bf16(128, D, true) | (1u << 15);  // A MN-major too
+  // dS: no swizzle, 8-key groups 128 bytes apart, blocks of 8 queries 2048
+  // bytes apart. K: as in the walks.
+  const uint64_t dA = sdesc_plain(smem_u32(smem), 128u, 2048u);
+  const uint64_t dB = sdesc(smem_u32(smem), 16384u, 1024u);
+  constexpr uint64_t kSlot = kDqSlotBytes >> 4;
+  uint32_t n_slot = 0, items = 0;
+  bool ok = true;
+  for (int k = 0; ok; ++k, ++items) {
+    const int idx = bwd_item(k);
+    if (idx >= p.n_g) break;
+    const BwdItem it = p.g_items[idx];
+    const uint32_t buf = items & 1u;
+    if (items >= 2 && !wait_warp(&ctl->acc_free[buf], ((items >> 1) - 1) & 1u, w, kBSiteAccFree))
+      break;
+    uint32_t started = 0;  // query tiles whose sum has begun
+    for (int n = it.lo; n < it.hi && ok; ++n) {
+      int at;
+      const int held = held_tiles(p, it, n, at);
+      if (!held) continue;
+      const uint32_t ks = n_slot % kDqSlots;
+      if (!wait_warp(&ctl->full[ks], (n_slot / kDqSlots) & 1u, w, kBSiteB0Full)) {
+        ok = false;
+        break;
+      }
+      ++n_slot;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (!ok || !((held >> q) & 1)) continue;
+        const uint32_t st = n_slot % kDqSlots;
+        if (!wait_warp(&ctl->full[st], (n_slot / kDqSlots) & 1u, w, kBSiteB1Full)) {
+          ok = false;
+          continue;
+        }
+        ++n_slot;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t d = tmem + (2 * buf + q) * D;
+          const uint64_t a = dA + st * kSlot, b = dB + ks * kSlot;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)  // 16 keys
+            mma_ss(d, a + x * (256u >> 4), b + x * (2048u >> 4), idesc,
+                   (x > 0 || ((started >> q) & 1u)) ? 1u : 0u);
+          mma_commit(&ctl->empty[st]);
+          if (q == 1 || !(held & 2)) mma_commit(&ctl->empty[ks]);
+        }
+        __syncwarp();
+      }
+      started |= held;
+    }
+    if (!ok) break;
+    if (elect_one()) mma_commit(&ctl->acc_full[buf]);
+    __syncwarp();
+  }
+  if (elect_one()) mma_commit(&ctl->drain);
+  __syncwarp();
+  wait_bounded(&ctl->drain, 0u, w, kBSiteDrain, false);
+}
+
+template <int D>
+__device__ void dq_epilogue(const BwdParams& p, DCtl* ctl, uint32_t tmem, const WaitCtx& w) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = warp >> 2, row = (warp & 3) * 32 + lane;
+  const uint32_t lane_bits = (uint32_t)((warp & 3) * 32) << 16;
+  const bool v8 = (reinterpret_cast<uintptr_t>(p.dq) & 31u) == 0;
+  uint32_t items = 0;
+  for (int k = 0;; ++k, ++items) {
+    const int idx = bwd_item(k);
+    if (idx >= p.n_g) return;
+    const BwdItem it = p.g_items[idx];
+    const SeqRec sr = p.seqs[it.b];
+    const uint32_t buf = items & 1u;
+    bool any = false;  // a key tile holds dS of this query tile
+    for (int n = it.lo; n < it.hi && !any; ++n) {
+      int at;
+      any = (held_tiles(p, it, n, at) >> q) & 1;
+    }
+    const int64_t i = ((int64_t)it.tile * 2 + q) * 128 + row;
+    const bool stored = i < sr.sq;
+    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.dq) + it.b * p.q_sb + it.h * p.q_sh +
+                       (sr.q_off + i) * p.q_st;
+    if (!wait_warp(&ctl->acc_full[buf], (items >> 1) & 1u, w, kBSiteAccFull)) return;
+    tc_fence_after();
+#pragma unroll 1
+    for (int ch = 0; ch < D / 32; ++ch) {
+      uint32_t ov[32];
+      tmem_ld32_wait(tmem + lane_bits + (2 * buf + q) * D + ch * 32, ov);
+      uint4 pk[4];
+      uint32_t* pw = reinterpret_cast<uint32_t*>(pk);
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        pw[c] = any ? pack_bf16(__uint_as_float(ov[2 * c]) * p.scale,
+                                __uint_as_float(ov[2 * c + 1]) * p.scale)
+                    : 0u;
+      if (stored) {
+        uint4* dst = reinterpret_cast<uint4*>(o + ch * 32);
+        if (v8) {
+          st_global_na_v8(dst, pk[0], pk[1]);
+          st_global_na_v8(dst + 2, pk[2], pk[3]);
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) st_global_na_v4(dst + v, pk[v]);
+        }
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->acc_free[buf]);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDqThreads, 1) fa_bwd_dq_sm100(const __grid_constant__ BwdParams p) {
+  using C = DCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  auto* ctl = reinterpret_cast<DCtl*>(smem + kDqSlots * kDqSlotBytes);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(p.err_word, kErrTimeout | (kBSiteSmem << kErrWhereShift));
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kDqSlots; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->acc_full[s], 1);
+      mbar_init(&ctl->acc_free[s], 8);
+    }
+    mbar_init(&ctl->fix, 1);
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile(
+        "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+            smem_u32(&ctl->tmem_base)),
+        "r"(C::kTmemCols)
+        : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+  const WaitCtx w{&ctl->abort_flag, p.err_word, p.timeout_ns};
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the key walk's dS
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp < 8) dq_epilogue<D>(p, ctl, tmem, w);
+  else if (warp == 8) dq_mma<D>(p, ctl, tmem, smem, w);
+  else dq_load<D>(p, ctl, smem, w);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(C::kTmemCols)
+                 : "memory");
+  }
 }
 
 }  // namespace dev
 
 // ----------------------------------------------------------------- host
 
-template <int D, bool kKeys, int kBias>
-static cudaError_t launch_walk(const BwdParams& p, int grid, bool early, cudaStream_t stream,
-                               const char** why) {
-  using C = dev::BCfg<D, kKeys>;
-  auto kern = dev::fa_bwd_sm100<D, kKeys, kBias>;
-  // Devices on which the kernel's attributes are set (one bit each).
-  static std::atomic<uint64_t> configured{0};
+// One launch with `threads` x `smem` of a kernel that splits `regs` registers
+// per thread; with `early` it may start before the launch ahead of it ends.
+template <typename Kernel>
+static cudaError_t launch_early(Kernel kern, std::atomic<uint64_t>* configured, const BwdParams& p,
+                                int grid, int threads, uint32_t smem, int regs, bool early,
+                                cudaStream_t stream, const char** why) {
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = device < 64 ? 1ull << device : 0ull;
-  if (!(configured.load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
+  const uint64_t bit = device < 64 ? 1ull << device : 0ull;  // devices with the attributes set
+  if (!(configured->load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes attr;
     e = cudaFuncGetAttributes(&attr, kern);
     if (e != cudaSuccess) return e;
     // setmaxnreg redistributes the registers the CTA was launched with; a split
     // larger than that allocation would never be granted.
-    if (attr.numRegs < 128) {
+    if (attr.numRegs < regs) {
       if (why) *why = "kernel compiled with fewer registers than its warpgroup split needs";
       return cudaErrorInvalidConfiguration;
     }
-    configured.fetch_or(bit);
+    configured->fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(dev::kBwdThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at = {};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = early ? 1 : 0;  // may start before the launch ahead of it ends
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int D, int kBias>
-static cudaError_t launch_both(const BwdParams& p, int num_sms, cudaStream_t stream,
+template <int D, bool kKeys, int kBias>
+static cudaError_t launch_walk(const BwdParams& p, int num_sms, cudaStream_t stream,
                                const char** why) {
-  if (p.n_q > 0) {
-    const cudaError_t e = launch_walk<D, false, kBias>(p, p.n_q < num_sms ? p.n_q : num_sms, true,
-                                                       stream, why);
-    if (e != cudaSuccess) return e;
-  }
-  if (p.n_k <= 0) return cudaSuccess;
-  return launch_walk<D, true, kBias>(p, p.n_k < num_sms ? p.n_k : num_sms, p.n_q > 0, stream, why);
+  const int n = kKeys ? p.n_k : p.n_q;
+  if (n <= 0) return cudaSuccess;
+  static std::atomic<uint64_t> configured{0};
+  return launch_early(dev::fa_bwd_sm100<D, kKeys, kBias>, &configured, p, n < num_sms ? n : num_sms,
+                      dev::kBwdThreads,
+                      dev::BCfg<D, kKeys, kBias == dev::kBwdBiasRel>::kSmemBytes,
+                      dev::kBwdRegsLaunch, p.n_q > 0, stream, why);
+}
+
+template <int D>
+static cudaError_t launch_dq(const BwdParams& p, int num_sms, cudaStream_t stream,
+                             const char** why) {
+  if (p.n_g <= 0) return cudaSuccess;
+  static std::atomic<uint64_t> configured{0};
+  return launch_early(dev::fa_bwd_dq_sm100<D>, &configured, p, p.n_g < num_sms ? p.n_g : num_sms,
+                      dev::kDqThreads, dev::DCfg<D>::kSmemBytes, 0, true, stream, why);
+}
+
+template <int D, int kBias>
+static cudaError_t launch_walks(const BwdParams& p, int num_sms, cudaStream_t stream,
+                                const char** why) {
+  cudaError_t e = p.ds ? cudaSuccess : launch_walk<D, false, kBias>(p, num_sms, stream, why);
+  if (e == cudaSuccess) e = launch_walk<D, true, kBias>(p, num_sms, stream, why);
+  if (e == cudaSuccess && p.ds) e = launch_dq<D>(p, num_sms, stream, why);
+  return e;
 }
 
 cudaError_t launch_bwd(int D, const BwdParams& p, int num_sms, cudaStream_t stream,
                        const char** why) {
   auto pick = [&](auto dim) {
     constexpr int kD = decltype(dim)::value;
-    if (p.rel.ext) return launch_both<kD, dev::kBwdBiasRel>(p, num_sms, stream, why);
-    if (p.slopes) return launch_both<kD, dev::kBwdBiasAlibi>(p, num_sms, stream, why);
-    return launch_both<kD, dev::kBwdBiasNone>(p, num_sms, stream, why);
+    if (p.rel.ext) return launch_walks<kD, dev::kBwdBiasRel>(p, num_sms, stream, why);
+    if (p.slopes) return launch_walks<kD, dev::kBwdBiasAlibi>(p, num_sms, stream, why);
+    return launch_walks<kD, dev::kBwdBiasNone>(p, num_sms, stream, why);
   };
   return D == 128 ? pick(std::integral_constant<int, 128>{}) : pick(std::integral_constant<int, 64>{});
 }

@@ -24,11 +24,21 @@ struct BwdState {
   std::vector<int64_t> key;
   bool valid = false;
   int32_t n_q = 0, n_k = 0;  // query and key items
-  int32_t tiles = 0;         // query tiles per head, over all sequences
+  int32_t n_g = 0;           // items of the dQ kernel
+  int32_t tiles = 0, k_tiles = 0;  // query and key tiles per head, over all sequences
+  // dS is written out (see launch_bwd) in these shares of the key and dQ
+  // lists, each of a bounded number of tiles; empty: it is not.
+  struct Chunk {
+    int32_t k0, k1, g0, g1;
+    int64_t tiles;
+  };
+  std::vector<Chunk> chunks;
+  bool no_spill = false;     // there was no room for dS
   SeqRec geo0{};             // geometry of sequence 0
   std::vector<uint8_t> host; // the uploaded lists
-  DeviceBuffer lists;        // [SeqRec x B][BwdItem x n_q][BwdItem x n_k]
+  DeviceBuffer lists;        // [SeqRec x B][BwdItem x n_q][x n_k][x n_g][KeySpan x k_tiles N]
   DeviceBuffer scratch;      // row statistics, dense-mask ranges, bias sums
+  DeviceBuffer spill;        // dS
 };
 
 // The bucket map of the relative position bias and the bias by distance.

@@ -47,6 +47,7 @@ def main():
     out.append(ld_fn("tmem_ld32_wait", 1))
     out.append(ld_fn("tmem_ld64_wait", 2))
     out.append(ld_fn("tmem_ld128_wait", 4))
+    out.append(st_fn(8))
     out.append(st_fn(16))
     out.append(st_fn(32))
     out += ["}  // namespace dev", "}  // namespace fa", ""]
