@@ -17,6 +17,7 @@
 
 #include "../../include/fa.h"
 #include "fa_handle.h"
+#include "fa_rows.h"
 #include "fa_kernel.h"
 #include "fa_plan.h"
 
@@ -225,6 +226,46 @@ fa_status_t refresh_plan(fa_handle_t h, const int64_t* prefix, const int64_t* cu
   h->n_items = (int32_t)items.size();
   h->n_seqs = (int32_t)recs.size();
   if (!recs.empty()) h->geo0 = recs[0];
+  h->max_rows = h->max_keys = 0;
+  for (const SeqRec& r : recs) {
+    h->max_rows = std::max(h->max_rows, r.sq);
+    h->max_keys = std::max(h->max_keys, r.skv);
+  }
+  return FA_OK;
+}
+
+// The forward with the learned bias for sequences of a few rows.
+fa_status_t forward_rows(fa_handle_t h, const void* q, const void* k, const void* v,
+                         const fa_relbias_t* bias, void* o, float* lse, cudaStream_t stream) {
+  const fa_desc_t* d = &h->desc;
+  RowsParams p;
+  std::memset(&p, 0, sizeof(p));
+  RelTable table;
+  fa_status_t st = prepare_rel(h, bias, stream, &p.rel, &table);
+  if (st != FA_OK) return st;
+  const int64_t groups = d->B * d->N;
+  p.splits = rows_splits(groups, h->max_keys, h->num_sms);
+  const size_t count = align_up((size_t)groups * sizeof(unsigned int), 256);
+  st = ensure_buffer(h, &h->rel.rows,
+                     count + (p.splits > 1 ? rows_part_bytes((int)d->D, groups, p.splits) : 0));
+  if (st != FA_OK) return st;
+  p.done = static_cast<unsigned int*>(h->rel.rows.ptr);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(h->rel.rows.ptr) + count);
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.o = o;
+  p.lse = lse;
+  p.seqs = reinterpret_cast<const SeqRec*>(static_cast<uint8_t*>(h->d_ws) + kHeaderBytes);
+  operand_strides(d, d->Sq, &p.q_sb, &p.q_sh, &p.q_st);
+  operand_strides(d, d->Skv, &p.k_sb, &p.k_sh, &p.k_st);
+  p.l_sb = d->layout == FA_TND ? 0 : d->N * d->Sq;
+  p.l_sh = d->Sq;
+  p.B = (int32_t)d->B;
+  p.N = (int32_t)d->N;
+  p.scale_log2 = (float)(d->scale * 1.4426950408889634073599);
+  const cudaError_t e = launch_rows((int)d->D, h->max_rows, p, table, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "few-row launch");
   return FA_OK;
 }
 
@@ -337,6 +378,14 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
   st = refresh_plan(h, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask, stream);
   if (st != FA_OK) return st;
   if (h->n_items == 0) return FA_OK;  // no query rows: nothing to write
+  if (bias && few_rows(h->max_rows, d->B * d->N, h->num_sms)) {
+    st = forward_rows(h, q, k, v, bias, o, lse, stream);
+    if (st != FA_OK) return st;
+    const cudaError_t er = cudaEventRecord(h->last_call, stream);
+    if (er != cudaSuccess) return cuda_fail(er, "cudaEventRecord");
+    h->any_call = true;
+    return FA_OK;
+  }
   st = encode_maps(h, q, k, v);
   if (st != FA_OK) return st;
 
@@ -425,7 +474,7 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
     RelTable table;
     st = prepare_rel(h, bias, stream, &p.rel, &table);
     if (st != FA_OK) return st;
-    const cudaError_t er = launch_rel_expand(table, stream);
+    const cudaError_t er = launch_rel_expand(table, nullptr, 0, stream);
     if (er != cudaSuccess) return cuda_fail(er, "bias expansion launch");
   }
   p.tnd = d->layout == FA_TND ? 1 : 0;

@@ -79,8 +79,9 @@ struct RelTable {
   float* ext;                // out: [N][4][rel_row(reach)]
   int32_t N, reach;
 };
-// Lays the table out by distance.
-cudaError_t launch_rel_expand(const RelTable& t, cudaStream_t stream);
+// Lays the table out by distance, and sets n_zero words at `zero` to 0.
+cudaError_t launch_rel_expand(const RelTable& t, unsigned int* zero, int64_t n_zero,
+                              cudaStream_t stream);
 
 // ------------------------------------------------------------- the backward
 struct __align__(64) BwdParams {

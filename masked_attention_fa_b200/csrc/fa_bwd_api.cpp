@@ -47,7 +47,8 @@ fa_status_t refuse_capture(cudaStream_t stream) {
 }
 
 void release_training(fa_handle_t h) {
-  for (DeviceBuffer* b : {&h->bwd.lists, &h->bwd.scratch, &h->bwd.spill, &h->rel.map, &h->rel.ext})
+  for (DeviceBuffer* b : {&h->bwd.lists, &h->bwd.scratch, &h->bwd.spill, &h->rel.map, &h->rel.ext,
+                          &h->rel.rows})
     if (b->ptr) cudaFree(b->ptr);
 }
 

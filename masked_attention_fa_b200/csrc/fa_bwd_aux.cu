@@ -38,7 +38,12 @@ __device__ __forceinline__ void expand_chunk(const RelTable& t, int h, int chunk
   }
 }
 
-__global__ void __launch_bounds__(256) rel_expand(RelTable t) { expand_chunk(t, blockIdx.y, blockIdx.x); }
+__global__ void __launch_bounds__(256) rel_expand(RelTable t, unsigned int* zero, int64_t n_zero) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t first = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+  for (int64_t x = first; x < n_zero; x += (int64_t)gridDim.x * gridDim.y * 256) zero[x] = 0u;
+  expand_chunk(t, blockIdx.y, blockIdx.x);
+}
 
 // One CTA per query tile, D / 8 threads per row (16-byte loads, whole rows
 // per group of threads): delta_i = sum_d do_id o_id.
@@ -221,8 +226,9 @@ cudaError_t launch_bwd_ranges(const BwdOccParams& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_rel_expand(const RelTable& t, cudaStream_t stream) {
-  rel_expand<<<dim3((rel_row(t.reach) + 255) / 256, t.N), 256, 0, stream>>>(t);
+cudaError_t launch_rel_expand(const RelTable& t, unsigned int* zero, int64_t n_zero,
+                              cudaStream_t stream) {
+  rel_expand<<<dim3((rel_row(t.reach) + 255) / 256, t.N), 256, 0, stream>>>(t, zero, n_zero);
   return cudaGetLastError();
 }
 

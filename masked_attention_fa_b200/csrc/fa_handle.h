@@ -46,6 +46,7 @@ struct RelState {
   std::vector<int32_t> bucket_of;
   DeviceBuffer map;
   DeviceBuffer ext;
+  DeviceBuffer rows;  // few-row forward: counters and partial results
 };
 
 }  // namespace fa
@@ -60,6 +61,7 @@ struct fa_handle_s {
   int32_t n_items = 0;
   int32_t n_seqs = 0;
   fa::SeqRec geo0{};  // geometry of sequence 0 (every sequence's, outside TND)
+  int32_t max_rows = 0, max_keys = 0;  // longest sequence of the plan
   // paged K/V calls: [header][SeqRec x B][PagedGroup x n_groups][PagedUnit x
   // n_units] then the units' partial results (the plan key starts with -2)
   int32_t n_groups = 0;
