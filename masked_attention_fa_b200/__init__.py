@@ -363,6 +363,13 @@ def fa_bwd_relbias(h, q, k, v, table, bucket_of, o, lse, d_o, dq, dk, dv, dtable
                                          _stream_int(stream, q.device)))
 
 
+def _raw_stream(index):
+    """Torch's current stream on CUDA device `index`, as an integer."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public call's time
+    return raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream_int(stream, device):
     import torch
     if type(stream) is int:
@@ -484,6 +491,9 @@ class MaskedAttention:
         self.desc = make_desc(layout, B, N, Sq, Skv, D, sparse_mode, pre_tokens, next_tokens,
                               scale, mask_kind, alibi)
         self.handle = fa_create(self.desc)
+        # What the calls compare and pass, worked out once.
+        self._lib = load_library()
+        (self._oshape, self._lshape), self._kshape = self.out_shapes(), self.kv_shape()
 
     def out_shapes(self):
         d = self.desc
@@ -540,16 +550,16 @@ class MaskedAttention:
                 FA_MASK_BNSS: (d.B, d.N, d.Sq, d.Skv)}.get(d.mask_kind)
 
     @staticmethod
-    def _need(device, shape, dtype, **tensors):
-        """Each given tensor: contiguous, of this dtype and shape, on `device`."""
-        import torch
-        for name, t in tensors.items():
-            if t is None:
-                continue
-            if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda
-                    or t.device != device or t.shape != shape or not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape "
-                                 f"{tuple(shape)} on {device}")
+    def _need(name, t, shape, dtype, device):
+        """t must be a contiguous tensor of this shape and dtype on `device`."""
+        try:
+            if (t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda
+                    and t.is_contiguous()):
+                return
+        except AttributeError:
+            pass
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape "
+                         f"{tuple(shape)} on {device}")
 
     def _need_bias(self, device, rel_bias, rel_buckets):
         import torch
@@ -557,7 +567,7 @@ class MaskedAttention:
             raise ValueError("rel_bias needs rel_buckets, its bucket map")
         if not isinstance(rel_bias, torch.Tensor) or rel_bias.dim() != 2:
             raise ValueError("rel_bias must be a tensor [num_buckets, N]")
-        self._need(device, (rel_bias.shape[0], self.desc.N), torch.float32, rel_bias=rel_bias)
+        self._need("rel_bias", rel_bias, (rel_bias.shape[0], self.desc.N), torch.float32, device)
 
     @staticmethod
     def _on(stream, device, inputs, body):
@@ -567,7 +577,7 @@ class MaskedAttention:
         stream has read them."""
         import torch
         if stream is None and torch.cuda.current_device() == device.index:
-            return body(torch.cuda.current_stream(device).cuda_stream)
+            return body(_raw_stream(device.index))
         with torch.cuda.device(device):
             here = torch.cuda.current_stream(device)
             if stream is None:
@@ -587,18 +597,25 @@ class MaskedAttention:
         import torch
         if atten_mask is not None or ranges is not None or slopes is not None:
             raise ValueError("rel_bias goes with neither atten_mask, ranges nor slopes")
-        oshape, lshape = self.out_shapes()
-        bf16, f32, dev = torch.bfloat16, torch.float32, q.device
-        self._need(dev, oshape, bf16, q=q, out=out)
-        self._need(dev, self.kv_shape(), bf16, k=k, v=v)
-        self._need(dev, lshape, f32, lse=lse)
+        bf16, f32, dev, need = torch.bfloat16, torch.float32, q.device, self._need
+        oshape, kshape, lshape = self._oshape, self._kshape, self._lshape
+        need("q", q, oshape, bf16, dev)
+        need("k", k, kshape, bf16, dev)
+        need("v", v, kshape, bf16, dev)
+        if out is not None:
+            need("out", out, oshape, bf16, dev)
+        if lse is not None:
+            need("lse", lse, lshape, f32, dev)
         self._need_bias(dev, rel_bias, rel_buckets)
 
         def body(s):
             o = torch.empty_like(q) if out is None else out
             l = torch.empty(lshape, dtype=f32, device=dev) if lse is None else lse
-            fa_fwd_relbias(self.handle, q, k, v, rel_bias, rel_buckets, o, l, prefix,
-                           actual_seq_qlen, actual_seq_kvlen, s)
+            a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
+            b, keep = _relbias(rel_bias, rel_buckets)
+            _check(self._lib.fa_fwd_relbias(
+                self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(b), *a.ptrs(),
+                o.data_ptr(), l.data_ptr(), s))
             return o, l
 
         return self._on(stream, dev, (q, k, v, rel_bias, out, lse), body)
@@ -611,36 +628,47 @@ class MaskedAttention:
         fa_bwd in include/fa.h). d_o, d_lse: the gradients of o and lse (d_lse
         None: 0)."""
         import torch
-        oshape, lshape = self.out_shapes()
-        bf16, f32, dev = torch.bfloat16, torch.float32, q.device
-        self._need(dev, oshape, bf16, q=q, o=o, d_o=d_o, dq=dq)
-        self._need(dev, self.kv_shape(), bf16, k=k, v=v, dk=dk, dv=dv)
-        self._need(dev, lshape, f32, lse=lse, d_lse=d_lse)
+        bf16, f32, dev, need = torch.bfloat16, torch.float32, q.device, self._need
+        oshape, kshape, lshape = self._oshape, self._kshape, self._lshape
+        need("q", q, oshape, bf16, dev)
+        need("o", o, oshape, bf16, dev)
+        need("d_o", d_o, oshape, bf16, dev)
+        need("k", k, kshape, bf16, dev)
+        need("v", v, kshape, bf16, dev)
+        need("lse", lse, lshape, f32, dev)
+        for name, t, shape, dtype in (("dq", dq, oshape, bf16), ("dk", dk, kshape, bf16),
+                                      ("dv", dv, kshape, bf16), ("d_lse", d_lse, lshape, f32)):
+            if t is not None:
+                need(name, t, shape, dtype, dev)
         if slopes is not None:
-            self._need(dev, (self.desc.N,), f32, slopes=slopes)
+            need("slopes", slopes, (self.desc.N,), f32, dev)
         if atten_mask is not None and self._mask_shape() is not None:
-            kind = atten_mask.dtype if atten_mask.dtype is torch.bool else torch.uint8
-            self._need(dev, self._mask_shape(), kind, atten_mask=atten_mask)
+            kind = torch.bool if getattr(atten_mask, "dtype", None) is torch.bool else torch.uint8
+            need("atten_mask", atten_mask, self._mask_shape(), kind, dev)
         if rel_bias is not None:
             if atten_mask is not None or slopes is not None:
                 raise ValueError("rel_bias goes with neither atten_mask nor slopes")
             self._need_bias(dev, rel_bias, rel_buckets)
-            self._need(dev, rel_bias.shape, f32, d_rel_bias=d_rel_bias)
+            if d_rel_bias is not None:
+                need("d_rel_bias", d_rel_bias, rel_bias.shape, f32, dev)
 
         def body(s):
             gq = torch.empty_like(q) if dq is None else dq
             gk = torch.empty_like(k) if dk is None else dk
             gv = torch.empty_like(v) if dv is None else dv
-            lens = (d_lse, prefix, actual_seq_qlen, actual_seq_kvlen, s)
+            a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
+            operands = (self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr())
+            rest = (o.data_ptr(), lse.data_ptr(), d_o.data_ptr(), _ptr(d_lse), *a.ptrs(),
+                    gq.data_ptr(), gk.data_ptr(), gv.data_ptr())
             if rel_bias is not None:
                 gt = torch.empty_like(rel_bias) if d_rel_bias is None else d_rel_bias
-                fa_bwd_relbias(self.handle, q, k, v, rel_bias, rel_buckets, o, lse, d_o, gq, gk,
-                               gv, gt, *lens)
+                b, keep = _relbias(rel_bias, rel_buckets)
+                _check(self._lib.fa_bwd_relbias(*operands, ctypes.byref(b), *rest, gt.data_ptr(), s))
                 return gq, gk, gv, gt
             if slopes is not None:
-                fa_bwd_alibi(self.handle, q, k, v, slopes, o, lse, d_o, gq, gk, gv, *lens)
+                _check(self._lib.fa_bwd_alibi(*operands, slopes.data_ptr(), *rest, s))
             else:
-                fa_bwd(self.handle, q, k, v, o, lse, d_o, gq, gk, gv, atten_mask, *lens)
+                _check(self._lib.fa_bwd(*operands, _ptr(atten_mask), *rest, s))
             return gq, gk, gv
 
         return self._on(stream, dev, (d_o, q, k, v, o, lse, atten_mask, d_lse, slopes, rel_bias, dq,

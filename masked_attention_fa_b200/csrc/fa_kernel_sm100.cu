@@ -1359,6 +1359,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_sm100(const __grid_constan
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   const WaitCtx w{&ctl->abort_flag, p.err_word, p.timeout_ns};
+  // What is above ran beside the launch that lays the bias out.
+  if constexpr (kBias == kBiasRel) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -1452,6 +1454,19 @@ static cudaError_t launch_d(const FwdParams& p, int grid, cudaStream_t stream, c
   if (!regs_ok) {
     if (why) *why = "kernel compiled with fewer registers than its warpgroup split needs";
     return cudaErrorInvalidConfiguration;
+  }
+  if constexpr (kBias == dev::kBiasRel) {  // may start before the bias is laid out
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(dev::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
   }
   kern<<<grid, dev::kThreads, C::kSmemBytes, stream>>>(p);
   return cudaGetLastError();
