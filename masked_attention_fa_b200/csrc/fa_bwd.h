@@ -97,7 +97,10 @@ struct __align__(64) BwdParams {
   // lse in log2 units (-inf for rows that see no key or are not stored, so
   // that their weights are 0 without a mask), then dlse - delta.
   float* stats;
-  const uint8_t* mask;       // dense attenMask, else null
+  // Dense attenMask, else null: one bit per pair, 1 = hidden, 32 keys of a
+  // query row or 32 query rows of a key to a word (see BwdMaskParams).
+  const uint32_t* bits_q;
+  const uint32_t* bits_k;
   unsigned int* err_word;
   const void* q;             // bf16 operands and gradients, one layout
   const void* k;
@@ -119,7 +122,8 @@ struct __align__(64) BwdParams {
   int64_t q_sb, q_sh, q_st;  // element strides of Q, O and their gradients
   int64_t k_sb, k_sh, k_st;  // of K, V and their gradients
   int64_t l_sb, l_sh;        // of lse
-  int64_t m_sb, m_sh, m_si;  // of the mask
+  int32_t m_sb, m_sh;        // mask plane = b * m_sb + h * m_sh
+  int32_t m_rows, m_keys;    // query rows and keys, rounded up to whole tiles
   int32_t alibi;             // fa_alibi_t
   int32_t n_q, n_k, n_g;     // items
   int32_t tnd;
@@ -127,9 +131,6 @@ struct __align__(64) BwdParams {
   uint64_t timeout_ns;
 };
 
-// Row statistics of every query tile (see BwdParams::stats), and with a bias
-// its layout by distance.
-cudaError_t launch_bwd_stats(int D, const BwdParams& p, cudaStream_t stream);
 // dQ, dK, dV and rel_part.
 //
 // Without p.ds by two walks that need nothing of each other: dQ by query tiles
@@ -142,20 +143,33 @@ cudaError_t launch_bwd_stats(int D, const BwdParams& p, cudaStream_t stream);
 cudaError_t launch_bwd(int D, const BwdParams& p, int num_sms, cudaStream_t stream,
                        const char** why);
 
-// Dense masks: copies the occupancy pre-pass's key-tile ranges into the
-// query items (and their union to the dQ kernel's items) and reduces its
-// classes to the key items' query-tile ranges and spans.
-struct BwdOccParams {
-  const TileRange* ranges;  // [plane][n_qt]
-  const uint8_t* cls;       // [plane][n_qt][n_kt]
+// Dense masks, one pass over the bytes: classifies every 128 x 128 tile of
+// every plane and packs it both ways,
+//     bits_q[plane][key / 32][row],   bits_k[plane][row / 32][key]
+// (rows and keys rounded up to whole tiles, pairs past the end hidden), so that
+// a thread of either walk reads one word per 32 pairs, next to its neighbours'.
+// Then gives the query, key and dQ items and the spans their ranges from the
+// classes: [lo, hi) from the first to the last tile with a visible pair, the
+// longest run of fully visible ones.
+struct BwdMaskParams {
+  const uint8_t* mask;   // [planes][Sq][Skv], nonzero = masked
+  uint32_t* bits_q;
+  uint32_t* bits_k;
+  uint8_t* cls;          // [plane][n_qt][n_kt], fa_tile_class_t
+  SeqRec geo;            // the geometry every sequence shares
   BwdItem* q_items;
   BwdItem* k_items;
   BwdItem* g_items;
   KeySpan* spans;
-  int64_t occ_sb, occ_sh;   // plane = b * occ_sb + h * occ_sh
+  int64_t planes;
+  int32_t m_sb, m_sh;    // plane = b * m_sb + h * m_sh
   int32_t n_q, n_k, n_g, n_qt, n_kt;
 };
-cudaError_t launch_bwd_ranges(const BwdOccParams& a, cudaStream_t stream);
+
+// Row statistics of every query tile (see BwdParams::stats), with a bias its
+// layout by distance, with a mask (planes > 0) the above.
+cudaError_t launch_bwd_stats(int D, const BwdParams& p, const BwdMaskParams& mask,
+                             cudaStream_t stream);
 
 // dtable[c][h] = the sum of rel_part over head h's key tiles (rows
 // [h * tiles, (h + 1) * tiles) of rel_part) and the distances of bucket c, in

@@ -306,13 +306,17 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   const BwdState& bw = h->bwd;
 
   // Scratch: row statistics | bias sums by tile and by distance, counters | the
-  // dense mask's ranges and classes.
+  // dense mask's bits both ways and classes.
   const size_t stat_bytes = align_up((size_t)bw.tiles * d->N * 256 * sizeof(float), 256);
   const size_t W = a.bias ? (size_t)rel_width(a.bias->reach) : 0;
   const size_t part_bytes = align_up((size_t)bw.k_tiles * d->N * W * sizeof(float), 256);
   const size_t dist_bytes = align_up((size_t)d->N * W * sizeof(double), 256);
   const int64_t planes = mask_planes(d, has_mask);
-  const size_t occ_bytes = planes ? occupancy_bytes(planes, d->Sq, d->Skv) : 0;
+  const int64_t m_rows = (int64_t)align_up((size_t)d->Sq, kTileM),
+                m_keys = (int64_t)align_up((size_t)d->Skv, kTileN);
+  const size_t bits_bytes = planes ? align_up((size_t)(planes * m_rows * m_keys / 8), 256) : 0;
+  const size_t occ_bytes =
+      planes ? 2 * bits_bytes + (size_t)(planes * (m_rows / kTileM) * (m_keys / kTileN)) : 0;
   const size_t done_bytes = a.bias ? align_up((size_t)d->N * sizeof(unsigned int), 256) : 0;
   st = ensure_buffer(h, &h->bwd.scratch,
                      stat_bytes + part_bytes + dist_bytes + done_bytes + occ_bytes);
@@ -382,42 +386,37 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
     p.rel_done = reinterpret_cast<unsigned int*>(scratch + stat_bytes + part_bytes + dist_bytes);
     p.rel_part = reinterpret_cast<float*>(scratch + stat_bytes);
   }
+  BwdMaskParams m;
+  std::memset(&m, 0, sizeof(m));
   if (has_mask) {
-    p.mask = a.atten_mask;
-    const int64_t plane = d->Sq * d->Skv;
-    p.m_si = d->Skv;
-    p.m_sb = d->mask_kind == FA_MASK_SS ? 0 : (d->mask_kind == FA_MASK_B1SS ? plane : d->N * plane);
-    p.m_sh = d->mask_kind == FA_MASK_BNSS ? plane : 0;
-    if (bw.n_q > 0 && bw.n_k > 0) {
-      OccParams oc;
-      std::memset(&oc, 0, sizeof(oc));
-      occupancy_shape(&oc, bw.geo0, planes);
-      oc.mask = a.atten_mask;
-      uint8_t* occ = scratch + stat_bytes + part_bytes + dist_bytes + done_bytes;
-      oc.ranges = reinterpret_cast<TileRange*>(occ);
-      oc.cls = occ + align_up((size_t)(oc.n_planes * oc.n_qt) * sizeof(TileRange), 256);
-      e = launch_occupancy(oc, h->num_sms, stream);
-      if (e != cudaSuccess) return cuda_fail(e, "occupancy pre-pass launch");
-      BwdOccParams r;
-      std::memset(&r, 0, sizeof(r));
-      r.ranges = oc.ranges;
-      r.cls = oc.cls;
-      r.q_items = q_items;
-      r.k_items = k_items;
-      r.g_items = g_items;
-      r.spans = spans;
-      r.occ_sb = d->mask_kind == FA_MASK_SS ? 0 : (d->mask_kind == FA_MASK_B1SS ? 1 : d->N);
-      r.occ_sh = d->mask_kind == FA_MASK_BNSS ? 1 : 0;
-      r.n_q = bw.n_q;
-      r.n_k = bw.n_k;
-      r.n_g = bw.n_g;
-      r.n_qt = oc.n_qt;
-      r.n_kt = oc.n_kt;
-      e = launch_bwd_ranges(r, stream);
-      if (e != cudaSuccess) return cuda_fail(e, "tile range launch");
-    }
+    uint8_t* occ = scratch + stat_bytes + part_bytes + dist_bytes + done_bytes;
+    m.mask = a.atten_mask;
+    m.bits_q = reinterpret_cast<uint32_t*>(occ);
+    m.bits_k = reinterpret_cast<uint32_t*>(occ + bits_bytes);
+    m.cls = occ + 2 * bits_bytes;
+    m.geo = bw.geo0;
+    m.q_items = q_items;
+    m.k_items = k_items;
+    m.g_items = g_items;
+    m.spans = spans;
+    m.planes = planes;
+    m.m_sb = d->mask_kind == FA_MASK_SS ? 0 : (d->mask_kind == FA_MASK_B1SS ? 1 : (int32_t)d->N);
+    m.m_sh = d->mask_kind == FA_MASK_BNSS ? 1 : 0;
+    m.n_q = bw.n_q;
+    m.n_k = bw.n_k;
+    m.n_g = bw.n_g;
+    m.n_qt = (int32_t)(m_rows / kTileM);
+    m.n_kt = (int32_t)(m_keys / kTileN);
+    if (planes * m.n_qt * m.n_kt > 0x7fffffff)
+      return fail(FA_ERR_UNSUPPORTED, "too many mask tiles");
+    p.bits_q = m.bits_q;
+    p.bits_k = m.bits_k;
+    p.m_sb = m.m_sb;
+    p.m_sh = m.m_sh;
+    p.m_rows = (int32_t)m_rows;
+    p.m_keys = (int32_t)m_keys;
   }
-  e = launch_bwd_stats((int)d->D, p, stream);
+  e = launch_bwd_stats((int)d->D, p, m, stream);
   if (e != cudaSuccess) return cuda_fail(e, "row statistics launch");
   const char* why = nullptr;
   if (ds_tiles > 0) {

@@ -45,14 +45,72 @@ __global__ void __launch_bounds__(256) rel_expand(RelTable t, unsigned int* zero
   expand_chunk(t, blockIdx.y, blockIdx.x);
 }
 
+// One CTA per tile; warp w takes the 32 x 32 blocks (w / 2, 2 (w % 2) + 0, 1):
+// lane l reads key l of every row, so that a vote gives a row's word and the
+// lane gathers its key's.
+__device__ __forceinline__ void mask_tile(const BwdMaskParams& a, int64_t tile) {
+  const int kt = (int)(tile % a.n_kt), qt = (int)(tile / a.n_kt % a.n_qt);
+  const int64_t plane = tile / a.n_kt / a.n_qt;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const SeqRec& s = a.geo;
+  const uint8_t* m = a.mask + plane * s.sq * (int64_t)s.skv;
+  const int64_t rows = (int64_t)a.n_qt * kTileM, keys = (int64_t)a.n_kt * kTileN;
+  const int row0 = qt * kTileM + (w >> 1) * 32;
+  bool any = false, full = true;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int key0 = kt * kTileN + ((w & 1) * 2 + y) * 32;
+    const int j = key0 + lane;
+    uint32_t hidden_row = 0u, hidden_key = 0u;
+    uint8_t v[32];
+    // Addresses are kept inside the mask, so that all loads are in flight.
+    const uint8_t* col = m + min(j, s.skv - 1);
+#pragma unroll
+    for (int r = 0; r < 32; ++r) v[r] = __ldg(col + (int64_t)min(row0 + r, s.sq - 1) * s.skv);
+    if (row0 + 32 > s.sq || key0 + 32 > s.skv) {
+#pragma unroll
+      for (int r = 0; r < 32; ++r)
+        if (row0 + r >= s.sq || j >= s.skv) v[r] = 1;
+    }
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const uint32_t word = __ballot_sync(0xffffffffu, v[r] != 0);
+      if (lane == r) hidden_row = word;
+      hidden_key |= (v[r] != 0 ? 1u : 0u) << r;
+    }
+    a.bits_q[(plane * (keys / 32) + key0 / 32) * rows + row0 + lane] = hidden_row;
+    a.bits_k[(plane * (rows / 32) + row0 / 32) * keys + j] = hidden_key;
+    // Row row0 + lane against the window of the geometry.
+    const int i = row0 + lane;
+    if (i < s.sq) {
+      const int64_t lo = imax64(row_lo(s, i) - key0, 0), hi = imin64(row_hi(s, i) - key0, 31);
+      uint32_t window = 0u;
+      if (lo <= hi) window = (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+      const uint32_t see = window & ~hidden_row;
+      any |= see != 0u;
+      full &= see == 0xffffffffu;
+    }
+  }
+  const int some = __syncthreads_or(any), all = __syncthreads_and(full);
+  if (threadIdx.x == 0)
+    a.cls[tile] = some ? (all ? FA_TILE_FULL : FA_TILE_PARTIAL) : FA_TILE_EMPTY;
+}
+
 // One CTA per query tile, D / 8 threads per row (16-byte loads, whole rows
 // per group of threads): delta_i = sum_d do_id o_id.
 template <int D>
-__global__ void __launch_bounds__(256) bwd_stats(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(256) bwd_stats(const __grid_constant__ BwdParams p,
+                                                 const __grid_constant__ BwdMaskParams a,
+                                                 int mask_tiles) {
   // The query walk may set itself up meanwhile.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if ((int)blockIdx.x >= p.n_q) {  // the CTAs past the query tiles lay the bias out
-    const int x = blockIdx.x - p.n_q, chunks = (rel_row(p.rel_table.reach) + 255) / 256;
+  if ((int)blockIdx.x < mask_tiles) {
+    mask_tile(a, blockIdx.x);
+    return;
+  }
+  const int block = blockIdx.x - mask_tiles;
+  if (block >= p.n_q) {  // the CTAs past the query tiles lay the bias out
+    const int x = block - p.n_q, chunks = (rel_row(p.rel_table.reach) + 255) / 256;
     if (x == 0)
       for (int h = threadIdx.x; h < p.rel_table.N; h += 256) p.rel_done[h] = 0u;
     expand_chunk(p.rel_table, x / chunks, x % chunks);
@@ -60,7 +118,7 @@ __global__ void __launch_bounds__(256) bwd_stats(const __grid_constant__ BwdPara
   }
   constexpr int L = D / 8;            // threads per row
   constexpr int R = 256 / L;          // rows per pass
-  const BwdItem it = p.q_items[blockIdx.x];
+  const BwdItem it = p.q_items[block];
   const SeqRec s = p.seqs[it.b];
   const int sl = threadIdx.x % L;
   const int64_t base = it.b * p.q_sb + it.h * p.q_sh;
@@ -98,43 +156,15 @@ __global__ void __launch_bounds__(256) bwd_stats(const __grid_constant__ BwdPara
   }
 }
 
-// Dense masks: thread n < n_q copies query item n's range, the n_g threads
-// after them join those of a dQ item, the warps after them reduce one key item each: [lo, hi) from the first to the last query
-// tile with a visible pair, and the longest run of fully visible ones (the
-// first on ties). A FULL class covers 128 stored keys.
-__global__ void __launch_bounds__(256) bwd_ranges(BwdOccParams a, int q_blocks) {
-  if ((int)blockIdx.x < q_blocks) {
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.n_q) {
-      const int m = n - a.n_q;
-      if (m >= a.n_g) return;
-      BwdItem it = a.g_items[m];
-      const TileRange* r = a.ranges + (it.b * a.occ_sb + it.h * a.occ_sh) * a.n_qt + it.tile * 2;
-      it.lo = it.hi = 0;
-      for (int x = 0; x < 2 && it.tile * 2 + x < a.n_qt; ++x) {
-        if (r[x].hi <= r[x].lo) continue;
-        it.lo = it.hi > 0 ? min(it.lo, r[x].lo) : r[x].lo;
-        it.hi = max(it.hi, r[x].hi);
-      }
-      a.g_items[m] = it;
-      return;
-    }
-    BwdItem it = a.q_items[n];
-    const TileRange r = a.ranges[(it.b * a.occ_sb + it.h * a.occ_sh) * a.n_qt + it.tile];
-    it.lo = r.lo, it.hi = r.hi, it.full_lo = r.full_lo, it.full_hi = r.full_hi;
-    a.q_items[n] = it;
-    return;
-  }
+// [lo, hi) and the longest run of FULL (the first on ties) of n classes
+// `stride` apart; the same in every lane of the warp.
+__device__ TileRange class_range(const uint8_t* cls, int n, int64_t stride) {
   const int lane = threadIdx.x & 31;
-  const int n = (blockIdx.x - q_blocks) * 8 + (threadIdx.x >> 5);
-  if (n >= a.n_k) return;
-  BwdItem it = a.k_items[n];
-  const uint8_t* cls = a.cls + (it.b * a.occ_sb + it.h * a.occ_sh) * a.n_qt * (int64_t)a.n_kt + it.tile;
   int lo = 0x7fffffff, hi = 0;
-  int best = 0, best_at = 0, run = 0;  // the same in every lane
-  for (int t0 = 0; t0 < a.n_qt; t0 += 32) {
+  int best = 0, best_at = 0, run = 0;
+  for (int t0 = 0; t0 < n; t0 += 32) {
     const int t = t0 + lane;
-    const int c = t < a.n_qt ? cls[(int64_t)t * a.n_kt] : 0;
+    const int c = t < n ? cls[t * stride] : FA_TILE_EMPTY;
     const uint32_t any = __ballot_sync(0xffffffffu, c != FA_TILE_EMPTY);
     const uint32_t full = __ballot_sync(0xffffffffu, c == FA_TILE_FULL);
     if (any) {
@@ -149,14 +179,54 @@ __global__ void __launch_bounds__(256) bwd_ranges(BwdOccParams a, int q_blocks) 
       }
     }
   }
-  if (lane != 0) return;
-  it.lo = hi > 0 ? lo : 0;
-  it.hi = hi;
-  it.full_lo = best > 0 ? best_at : it.lo;
-  it.full_hi = best > 0 ? best_at + best : it.lo;
-  a.k_items[n] = it;
-  a.spans[it.span].lo = it.lo;
-  a.spans[it.span].hi = it.hi;
+  TileRange r;
+  r.lo = hi > 0 ? lo : 0;
+  r.hi = hi;
+  r.full_lo = best > 0 ? best_at : r.lo;
+  r.full_hi = best > 0 ? best_at + best : r.lo;
+  return r;
+}
+
+// One warp per item: query items, key items (and their spans), dQ items.
+__global__ void __launch_bounds__(256) bwd_ranges(BwdMaskParams a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  int n = blockIdx.x * 8 + (threadIdx.x >> 5);
+  auto plane = [&](const BwdItem& it) {
+    return a.cls + (int64_t)(it.b * a.m_sb + it.h * a.m_sh) * a.n_qt * a.n_kt;
+  };
+  auto put = [&](BwdItem* at, const TileRange& r) {
+    at->lo = r.lo, at->hi = r.hi, at->full_lo = r.full_lo, at->full_hi = r.full_hi;
+  };
+  if (n < a.n_q) {
+    const BwdItem it = a.q_items[n];
+    const TileRange r = class_range(plane(it) + (int64_t)it.tile * a.n_kt, a.n_kt, 1);
+    if (lane == 0) put(a.q_items + n, r);
+    return;
+  }
+  n -= a.n_q;
+  if (n < a.n_k) {
+    const BwdItem it = a.k_items[n];
+    const TileRange r = class_range(plane(it) + it.tile, a.n_qt, a.n_kt);
+    if (lane == 0) {
+      put(a.k_items + n, r);
+      a.spans[it.span].lo = r.lo;
+      a.spans[it.span].hi = r.hi;
+    }
+    return;
+  }
+  n -= a.n_k;
+  if (n < a.n_g) {
+    const BwdItem it = a.g_items[n];
+    TileRange u{0, 0, 0, 0};
+    for (int x = 0; x < 2 && it.tile * 2 + x < a.n_qt; ++x) {
+      const TileRange r = class_range(plane(it) + (int64_t)(it.tile * 2 + x) * a.n_kt, a.n_kt, 1);
+      if (r.hi <= r.lo) continue;
+      u.lo = u.hi > 0 ? min(u.lo, r.lo) : r.lo;
+      u.hi = max(u.hi, r.hi);
+    }
+    if (lane == 0) put(a.g_items + n, u);
+  }
 }
 
 // dist[h][e] = sum over head h's key tiles, in 64 bits: one CTA per head and
@@ -170,8 +240,9 @@ __global__ void __launch_bounds__(256) rel_reduce(const float* __restrict__ part
                                                   float* __restrict__ dtable, int N, int tiles,
                                                   int reach, int num_buckets) {
   __shared__ double sm[8][32];
-  __shared__ double by_dist[2 * kRelMaxReach + 1 + 2 * kRelPad];
-  __shared__ int32_t bucket[2 * kRelMaxReach + 1 + 2 * kRelPad];
+  constexpr int kRoom = (2 * kRelMaxReach + 1 + 2 * kRelPad + 127) / 128 * 128;
+  __shared__ float by_dist[kRoom];
+  __shared__ int32_t bucket[kRoom];
   __shared__ bool last;
   const int W = rel_width(reach);
   const int h = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -194,35 +265,39 @@ __global__ void __launch_bounds__(256) rel_reduce(const float* __restrict__ part
   __syncthreads();
   if (!last) return;
   __threadfence();
-  for (int e = threadIdx.x; e < W; e += 256) {
-    by_dist[e] = __ldcg(dist + (int64_t)h * W + e);
-    bucket[e] = bucket_of[min(max(e - kRelPad, 0), 2 * reach)];
+  const int padded = (W + 127) / 128 * 128;
+  for (int e = threadIdx.x; e < padded; e += 256) {
+    by_dist[e] = e < W ? (float)__ldcg(dist + (int64_t)h * W + e) : 0.f;
+    bucket[e] = e < W ? bucket_of[min(max(e - kRelPad, 0), 2 * reach)] : -1;
   }
   __syncthreads();
   for (int c = w; c < num_buckets; c += 8) {
-    double a = 0.0;
-    for (int e = lane; e < W; e += 32)
-      if (bucket[e] == c) a += by_dist[e];
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int e = lane; e < padded; e += 128)
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) a += __shfl_xor_sync(0xffffffffu, a, x);
-    if (lane == 0) dtable[(int64_t)c * N + h] = (float)a;
+      for (int y = 0; y < 4; ++y) a[y] += bucket[e + 32 * y] == c ? by_dist[e + 32 * y] : 0.f;
+    float sum = (a[0] + a[1]) + (a[2] + a[3]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    if (lane == 0) dtable[(int64_t)c * N + h] = sum;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_bwd_stats(int D, const BwdParams& p, cudaStream_t stream) {
+cudaError_t launch_bwd_stats(int D, const BwdParams& p, const BwdMaskParams& mask,
+                             cudaStream_t stream) {
   if (p.n_q <= 0) return cudaSuccess;
-  const int grid =
-      p.n_q + (p.rel.ext ? (rel_row(p.rel_table.reach) + 255) / 256 * p.rel_table.N : 0);
-  if (D == 128) bwd_stats<128><<<grid, 256, 0, stream>>>(p);
-  else bwd_stats<64><<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_bwd_ranges(const BwdOccParams& a, cudaStream_t stream) {
-  const int qb = (a.n_q + a.n_g + 255) / 256, kb = (a.n_k + 7) / 8;
-  if (qb + kb > 0) bwd_ranges<<<qb + kb, 256, 0, stream>>>(a, qb);
+  const int64_t tiles = mask.planes * mask.n_qt * mask.n_kt;
+  const int64_t grid =
+      tiles + p.n_q + (p.rel.ext ? (rel_row(p.rel_table.reach) + 255) / 256 * p.rel_table.N : 0);
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  if (D == 128) bwd_stats<128><<<(int)grid, 256, 0, stream>>>(p, mask, (int)tiles);
+  else bwd_stats<64><<<(int)grid, 256, 0, stream>>>(p, mask, (int)tiles);
+  if (tiles > 0) {
+    const int64_t items = (int64_t)mask.n_q + mask.n_k + mask.n_g;
+    bwd_ranges<<<(int)((items + 7) / 8), 256, 0, stream>>>(mask);
+  }
   return cudaGetLastError();
 }
 

@@ -332,17 +332,6 @@ __device__ __forceinline__ uint64_t sdesc_plain(uint32_t addr, uint32_t lbo, uin
   return sdesc(addr, lbo, sbo) & ~(7ull << 61);
 }
 
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 // D[128 x 128] = A B^T, both K-major over the head dim; A in shared memory
 // (key walk) or tensor memory.
 template <int D, bool kKeys, bool kRel>
@@ -556,11 +545,14 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
         v_hi = (int)imax64(imin64(sr.skv - 1, row_hi(sr, at)), -1);
       }
     }
-    const uint8_t* mrow = nullptr;  // the mask from this row's entry of column 0
+    // This row's words of the mask, one per 32 columns, m_step apart.
+    const uint32_t* mrow = nullptr;
     int64_t m_step = 0;
-    if ((sr.flags & kSeqDenseMask) && stored) {
-      mrow = p.mask + it.b * p.m_sb + it.h * p.m_sh + (kKeys ? at : at * p.m_si);
-      m_step = kKeys ? p.m_si : 1;
+    if (sr.flags & kSeqDenseMask) {
+      m_step = kKeys ? p.m_keys : p.m_rows;
+      const int64_t plane = it.b * p.m_sb + it.h * p.m_sh;
+      mrow = (kKeys ? p.bits_k : p.bits_q) +
+             plane * ((kKeys ? p.m_rows : p.m_keys) / 32) * m_step + at;
     }
     float nl = 0.f, nd = 0.f;
     if constexpr (!kKeys) {
@@ -593,15 +585,9 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
       if (partial) {
         interval_bits(v_lo - c0, v_hi - c0, wm);
         if (mrow != nullptr) {
-          const uint8_t* mt = mrow + c0 * m_step;
 #pragma unroll
-          for (int wd = 0; wd < kCols / 32; ++wd) {
-            uint32_t see = wm[wd], hide = 0u;
-#pragma unroll 8
-            for (int c = 0; c < 32; ++c)
-              if (((see >> c) & 1u) && __ldg(mt + (wd * 32 + c) * m_step) != 0) hide |= 1u << c;
-            wm[wd] = see & ~hide;
-          }
+          for (int wd = 0; wd < kCols / 32; ++wd)
+            wm[wd] &= ~__ldg(mrow + (c0 / 32 + wd) * m_step);
         }
       }
       const float* st = reinterpret_cast<const float*>(sStat + (n & 1u) * 1024u) + kCols * g;

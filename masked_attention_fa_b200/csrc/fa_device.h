@@ -162,6 +162,17 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle (SM100 layout type 2,
 // descriptor version 1). Byte offsets lbo/sbo as the canonical layouts use:
 //   K-major:  rows 128 B apart, 8-row groups sbo = 1024 B apart (lbo unused);
