@@ -125,6 +125,8 @@ struct __align__(64) BwdParams {
   int32_t m_sb, m_sh;        // mask plane = b * m_sb + h * m_sh
   int32_t m_rows, m_keys;    // query rows and keys, rounded up to whole tiles
   int32_t alibi;             // fa_alibi_t
+  unsigned int* claims;      // claimed items of the three lists, 0 at the start
+  int32_t n_claims;          // words to set to 0 with the statistics
   int32_t n_q, n_k, n_g;     // items
   int32_t tnd;
   float scale, scale_log2;

@@ -114,7 +114,8 @@ int64_t spill_tiles() {
 // Items without a tile first (their zeros are written beside the first items'
 // products), then longest first, in buckets of similar length inside which the
 // items of one (sequence, head) stand together: the tiles in flight then share
-// their operands through L2 (see order_work_list).
+// their operands through L2 (see order_work_list). The kernels claim them in
+// this order.
 void order_items(std::vector<BwdItem>::iterator first, std::vector<BwdItem>::iterator last,
                  int num_sms) {
   const int32_t bucket = claims_items(last - first, num_sms) ? kLocalityTiles : 1;
@@ -305,8 +306,8 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   }
   const BwdState& bw = h->bwd;
 
-  // Scratch: row statistics | bias sums by tile and by distance, counters | the
-  // dense mask's bits both ways and classes.
+  // Scratch: row statistics | bias sums by tile and by distance, counters |
+  // claim counters | the dense mask's bits both ways and classes.
   const size_t stat_bytes = align_up((size_t)bw.tiles * d->N * 256 * sizeof(float), 256);
   const size_t W = a.bias ? (size_t)rel_width(a.bias->reach) : 0;
   const size_t part_bytes = align_up((size_t)bw.k_tiles * d->N * W * sizeof(float), 256);
@@ -318,8 +319,10 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   const size_t occ_bytes =
       planes ? 2 * bits_bytes + (size_t)(planes * (m_rows / kTileM) * (m_keys / kTileN)) : 0;
   const size_t done_bytes = a.bias ? align_up((size_t)d->N * sizeof(unsigned int), 256) : 0;
+  const size_t n_claims = 3 * std::max<size_t>(1, bw.chunks.size());
+  const size_t claim_bytes = align_up(n_claims * sizeof(unsigned int), 256);
   st = ensure_buffer(h, &h->bwd.scratch,
-                     stat_bytes + part_bytes + dist_bytes + done_bytes + occ_bytes);
+                     stat_bytes + part_bytes + dist_bytes + done_bytes + claim_bytes + occ_bytes);
   if (st != FA_OK) return st;
   uint8_t* scratch = static_cast<uint8_t*>(bw.scratch.ptr);
   uint8_t* lists = static_cast<uint8_t*>(bw.lists.ptr);
@@ -389,7 +392,7 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   BwdMaskParams m;
   std::memset(&m, 0, sizeof(m));
   if (has_mask) {
-    uint8_t* occ = scratch + stat_bytes + part_bytes + dist_bytes + done_bytes;
+    uint8_t* occ = scratch + stat_bytes + part_bytes + dist_bytes + done_bytes + claim_bytes;
     m.mask = a.atten_mask;
     m.bits_q = reinterpret_cast<uint32_t*>(occ);
     m.bits_k = reinterpret_cast<uint32_t*>(occ + bits_bytes);
@@ -416,7 +419,10 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
     p.m_rows = (int32_t)m_rows;
     p.m_keys = (int32_t)m_keys;
   }
-  e = launch_bwd_stats((int)d->D, p, m, stream);
+  p.claims = reinterpret_cast<unsigned int*>(scratch + stat_bytes + part_bytes + dist_bytes + done_bytes);
+  p.n_claims = (int32_t)n_claims;
+  e = p.n_q > 0 ? launch_bwd_stats((int)d->D, p, m, stream)
+                : cudaMemsetAsync(p.claims, 0, n_claims * sizeof(unsigned int), stream);
   if (e != cudaSuccess) return cuda_fail(e, "row statistics launch");
   const char* why = nullptr;
   if (ds_tiles > 0) {
@@ -427,6 +433,7 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
       p.n_k = ch.k1 - ch.k0;
       p.g_items = g_items + ch.g0;
       p.n_g = ch.g1 - ch.g0;
+      if (c > 0) p.claims += 3;
       e = launch_bwd((int)d->D, p, h->num_sms, stream, &why);
     }
   } else {

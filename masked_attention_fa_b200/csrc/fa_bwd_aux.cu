@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(256) bwd_stats(const __grid_constant__ BwdPara
     return;
   }
   const int block = blockIdx.x - mask_tiles;
+  if (block == 0)
+    for (int x = threadIdx.x; x < p.n_claims; x += 256) p.claims[x] = 0u;
   if (block >= p.n_q) {  // the CTAs past the query tiles lay the bias out
     const int x = block - p.n_q, chunks = (rel_row(p.rel_table.reach) + 255) / 256;
     if (x == 0)

@@ -78,7 +78,8 @@ enum BwdSite : uint32_t {
   kBSiteB0Empty = 32, kBSiteB1Empty, kBSiteStatEmpty, kBSiteA0Empty, kBSiteA1Empty, kBSiteFix,
   kBSiteB0Full, kBSiteB1Full, kBSiteStatFull, kBSiteA0Full, kBSiteA1Full, kBSiteSFull, kBSiteSFree,
   kBSitePFull, kBSiteDpFull, kBSiteDsFull, kBSiteAccFull, kBSiteAccFree, kBSiteSumFull,
-  kBSiteSumEmpty, kBSiteFarFull, kBSiteFarEmpty, kBSiteDrain, kBSiteSmem,
+  kBSiteSumEmpty, kBSiteFarFull, kBSiteFarEmpty, kBSiteDrain, kBSiteSmem, kBSiteIdxFull,
+  kBSiteIdxEmpty,
 };
 
 template <int D, bool kKeys, bool kRel>
@@ -106,6 +107,8 @@ struct BCfg {
   static_assert(kColAcc1 + D <= kTmemCols && kColA1 + D / 2 <= kTmemCols, "tensor memory budget");
 };
 
+constexpr int kBwdIdxSlots = 4;
+
 struct BCtl {
   uint64_t b0_full[4], b0_empty[4], b1_full[4], b1_empty[4];
   uint64_t stat_full[2], stat_empty[2];  // key walk: the query tile's row statistics
@@ -117,6 +120,8 @@ struct BCtl {
   uint64_t acc_full[2], acc_free[2];
   uint64_t sum_full[2], sum_empty[2];    // bias gradient: sums by diagonal of one tile
   uint64_t far_full, far_empty;          // ... and of the tiles past the reach
+  uint64_t idx_full[kBwdIdxSlots], idx_empty[kBwdIdxSlots];  // claimed items
+  int idx_ring[kBwdIdxSlots];
   uint64_t drain;
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -178,11 +183,49 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// k-th item of this CTA: the lists are in descending order of length and
-// dealt out in a snake, which evens out the per-CTA sums.
-__device__ __forceinline__ int bwd_item(int k) {
-  const int G = gridDim.x, c = blockIdx.x;
-  return k * G + ((k & 1) ? (G - 1 - c) : c);
+// Items are claimed at run time, in list order (longest first): CTA c starts
+// with item c, every later one is the next that no CTA has taken. The load warp
+// claims each once the loads of the one before are under way and passes its
+// index on through a ring; it ends with one past the list.
+template <typename Ctl>
+__device__ __forceinline__ int bwd_claim(Ctl* ctl, unsigned int* counter, int k, const WaitCtx& w) {
+  const int slot = k % kBwdIdxSlots;
+  if (k >= kBwdIdxSlots &&
+      !wait_warp(&ctl->idx_empty[slot], ((k / kBwdIdxSlots) - 1) & 1u, w, kBSiteIdxEmpty))
+    return 0x7fffffff;
+  int idx = blockIdx.x;
+  if ((threadIdx.x & 31) == 0) {
+    if (k > 0) idx = (int)(gridDim.x + atomicAdd(counter, 1u));  // below items + 2 gridDim.x
+    ctl->idx_ring[slot] = idx;
+    mbar_arrive(&ctl->idx_full[slot]);
+  }
+  return __shfl_sync(0xffffffffu, idx, 0);
+}
+
+// The CTA's k-th item (whole warps of the other roles); past any list when the
+// wait gave up.
+template <typename Ctl>
+__device__ __forceinline__ int bwd_take(Ctl* ctl, int k, const WaitCtx& w) {
+  const int slot = k % kBwdIdxSlots;
+  if (!wait_warp(&ctl->idx_full[slot], (k / kBwdIdxSlots) & 1u, w, kBSiteIdxFull))
+    return 0x7fffffff;
+  const int idx = *reinterpret_cast<volatile int*>(&ctl->idx_ring[slot]);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl->idx_empty[slot]);
+  return idx;
+}
+
+// Whether the phase with the given parity is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
 }
 
 // The CTA's steps in order: tile t of an item that has tiles. The query walk
@@ -194,19 +237,26 @@ struct Step {
   bool valid, first, last;
 };
 
+// Moves to the next step, over items without tiles. With `block` false it does
+// not wait for items that are not claimed yet: false, and the step is unchanged
+// but for what has been passed over.
 template <bool kKeys>
-__device__ __forceinline__ void next_step(const BwdItem* items, int n, Step& s) {
+__device__ __forceinline__ bool next_step(const BwdItem* items, int n, BCtl* ctl, const WaitCtx& w,
+                                          Step& s, bool block) {
   if (s.valid && !s.last) {
     s.t += kKeys ? -1 : 1;
     s.first = false;
     s.last = kKeys ? s.t == s.lo : s.t + 1 == s.hi;
-    return;
+    return true;
   }
   for (;;) {
-    const int idx = bwd_item(s.k);
+    if (!block && !__all_sync(0xffffffffu, mbar_test(&ctl->idx_full[s.k % kBwdIdxSlots],
+                                                     (s.k / kBwdIdxSlots) & 1u)))
+      return false;
+    const int idx = bwd_take(ctl, s.k, w);
     if (idx >= n) {
       s.valid = false;
-      return;
+      return true;
     }
     ++s.k;
     const int4 r = __ldg(reinterpret_cast<const int4*>(items + idx) + 1);  // lo, hi, full range
@@ -216,7 +266,7 @@ __device__ __forceinline__ void next_step(const BwdItem* items, int n, Step& s) 
     s.t = kKeys ? s.hi - 1 : s.lo;
     s.valid = s.first = true;
     s.last = s.lo + 1 == s.hi;
-    return;
+    return true;
   }
 }
 
@@ -272,7 +322,8 @@ __device__ void bwd_load(const BwdParams& p, BCtl* ctl, uint8_t* sA, uint8_t* sB
     return true;
   };
   for (int k = 0; ok; ++k) {
-    const int idx = bwd_item(k);
+    const int idx = bwd_claim(ctl, p.claims + (kKeys ? 1 : 0), k, w);
+    if (idx == 0x7fffffff) ok = false;
     if (idx >= n_items) break;
     const BwdItem it = items[idx];
     if (it.hi <= it.lo) continue;
@@ -385,7 +436,7 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
   Step cur, nx;
   nx.k = 0;
   nx.valid = false;
-  next_step<kKeys>(items, n_items, nx);
+  next_step<kKeys>(items, n_items, ctl, w, nx, true);
   uint32_t n = 0;       // step of nx
   uint32_t a0 = 0, a1 = 0;  // held operands awaited
   uint32_t items_done = 0;
@@ -426,9 +477,12 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
   while (ok && nx.valid) {
     cur = nx;
     const uint32_t c = n;
-    next_step<kKeys>(items, n_items, nx);
+    // The item behind this one may not be claimed yet (items without tiles in
+    // between need every role to pass them, the epilogue among them, which
+    // waits for this item's products): then its products come after this one's.
+    const bool late = !next_step<kKeys>(items, n_items, ctl, w, nx, false);
     ++n;
-    if (nx.valid && !operands0()) break;
+    if (!late && nx.valid && !operands0()) break;
     if constexpr (kKeys) {
       // dV in two halves of the queries: the first while the other half's P
       // is computed.
@@ -445,7 +499,7 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
         tc_fence_after();
         if (elect_one()) {
           issue_acc<D>(tmem + C::kColAcc1, tS, dM1 + st * kSlot,
-                              (cur.first && half == 0) ? 0u : 1u, half);
+                       (cur.first && half == 0) ? 0u : 1u, half);
           if (half) {
             mma_commit(&ctl->b1_empty[st]);
             if (cur.last) mma_commit(&ctl->acc_full[1]);
@@ -454,13 +508,13 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
         __syncwarp();
       }
       if (!ok) break;
-      if (nx.valid) scores();
-    } else if (nx.valid) {
+      if (!late && nx.valid) scores();
+    } else if (!late && nx.valid) {
       if (!wait_warp(&ctl->s_free, c & 1u, w, kBSiteSFree)) break;
       tc_fence_after();
       scores();
     }
-    if (nx.valid && !operands1()) break;
+    if (!late && nx.valid && !operands1()) break;
     if (cur.first && items_done > 0 &&
         !wait_warp(&ctl->acc_free[0], (items_done - 1) & 1u, w, kBSiteAccFree))
       break;
@@ -475,6 +529,14 @@ __device__ void bwd_mma(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uint
     }
     __syncwarp();
     if (cur.last) ++items_done;
+    if (late) {
+      next_step<kKeys>(items, n_items, ctl, w, nx, true);
+      if (!nx.valid) break;
+      if (!operands0() || !operands1()) break;
+      if (!kKeys && !wait_warp(&ctl->s_free, c & 1u, w, kBSiteSFree)) break;
+      tc_fence_after();
+      scores();
+    }
     if (nx.valid) dprobs();
   }
   // Wait until every product issued here (and its commits) has finished with
@@ -526,7 +588,7 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
   uint32_t n_near = 0, n_far = 0;
   bool ok = true;
   for (int k = 0; ok; ++k) {
-    const int idx = bwd_item(k);
+    const int idx = bwd_take(ctl, k, w);
     if (idx >= n_items) break;
     const BwdItem it = items[idx];
     if (it.hi <= it.lo) continue;
@@ -832,7 +894,7 @@ __device__ void bwd_sums(const BwdParams& p, BCtl* ctl, const float* sSum, const
   const int width = rel_width(p.rel.reach);
   uint32_t n_near = 0, n_far = 0;
   for (int k = 0;; ++k) {
-    const int idx = bwd_item(k);
+    const int idx = bwd_take(ctl, k, w);
     if (idx >= p.n_k) return;
     const BwdItem it = p.k_items[idx];
     float* out = p.rel_part + (int64_t)it.span * width;
@@ -944,16 +1006,6 @@ __device__ void bwd_epilogue(const BwdParams& p, BCtl* ctl, uint32_t tmem, const
     __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(dst) + it.b * sb + it.h * sh +
                        ((int64_t)(kKeys ? sr.kv_off : sr.q_off) + at) * st;
     const bool v8 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
-    if (it.hi <= it.lo) {
-      // Zeros, whole rows per group of lanes.
-      constexpr int kLanes = D / 8;
-      const int rows = min(128, (kKeys ? sr.skv : sr.sq) - it.tile * 128);
-#pragma unroll 4
-      for (int r = wq * 32 + lane / kLanes; r < min(rows, wq * 32 + 32); r += 32 / kLanes)
-        st_global_na_v4(reinterpret_cast<uint4*>(o + (int64_t)(r - row) * st) + lane % kLanes,
-                        make_uint4(0u, 0u, 0u, 0u));
-      return true;
-    }
     if (!wait_warp(&ctl->acc_full[which], done & 1u, w, kBSiteAccFull)) return false;
     tc_fence_after();
     const uint32_t src = tmem + lane_bits + (which ? C::kColAcc1 : C::kColAcc0);
@@ -982,32 +1034,47 @@ __device__ void bwd_epilogue(const BwdParams& p, BCtl* ctl, uint32_t tmem, const
     if (lane == 0) mbar_arrive(&ctl->acc_free[which]);
     return true;
   };
-  int ahead = 0;  // list position from which the next item with tiles is looked for
-  auto fetch_next = [&]() -> bool {
-    if constexpr (!kKeys) {
-      for (int idx; (idx = bwd_item(ahead)) < n_items;) {
-        ++ahead;
-        const BwdItem it = items[idx];
-        if (it.hi > it.lo) return fetch(it);
-      }
-    }
-    return true;
-  };
-  if (!fetch_next()) return;
-  for (int k = 0;; ++k) {
-    const int idx = bwd_item(k);
-    if (idx >= n_items) break;
-    const BwdItem it = items[idx];
+  // Zeros for an item without a tile, whole rows per group of lanes.
+  auto zero = [&](const BwdItem& it, void* dst) {
+    constexpr int kLanes = D / 8;
     const SeqRec sr = p.seqs[it.b];
-    const bool live = it.hi > it.lo;
-    if (live && !fetch_next()) return;
+    const int rows = min(128, (kKeys ? sr.skv : sr.sq) - it.tile * 128);
+    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(dst) + it.b * sb + it.h * sh +
+                       ((int64_t)(kKeys ? sr.kv_off : sr.q_off) + it.tile * 128) * st;
+#pragma unroll 4
+    for (int r = wq * 32 + lane / kLanes; r < min(rows, wq * 32 + 32); r += 32 / kLanes)
+      st_global_na_v4(reinterpret_cast<uint4*>(o + (int64_t)r * st) + lane % kLanes,
+                      make_uint4(0u, 0u, 0u, 0u));
+  };
+  // The next item with tiles (those without are dealt with on the way), its
+  // operands brought in; past the list at its end, -1 when a wait gave up.
+  int k = 0;
+  auto next_item = [&]() -> int {
+    for (;; ++k) {
+      const int idx = bwd_take(ctl, k, w);
+      if (idx >= n_items) return idx;
+      const BwdItem it = items[idx];
+      if (it.hi > it.lo) {
+        ++k;
+        if (!kKeys && !fetch(it)) return -1;
+        return idx;
+      }
+      zero(it, kKeys ? p.dk : p.dq);
+      if (kKeys) zero(it, p.dv);
+    }
+  };
+  for (int cur = next_item(); cur >= 0 && cur < n_items; ++done) {
+    const BwdItem it = items[cur];
+    const SeqRec sr = p.seqs[it.b];
     if constexpr (kKeys) {
       if (!store_acc(it, sr, 1, p.dv, 1.f)) return;
       if (!store_acc(it, sr, 0, p.dk, p.scale)) return;
+      cur = next_item();
     } else {
-      if (!store_acc(it, sr, 0, p.dq, p.scale)) return;
+      const int next = next_item();
+      if (next < 0 || !store_acc(it, sr, 0, p.dq, p.scale)) return;
+      cur = next;
     }
-    if (live) ++done;
   }
 }
 
@@ -1042,6 +1109,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
       mbar_init(&ctl->acc_free[s], 4);
       mbar_init(&ctl->sum_full[s], kMathWarps);
       mbar_init(&ctl->sum_empty[s], 1);
+    }
+    for (int s = 0; s < kBwdIdxSlots; ++s) {
+      mbar_init(&ctl->idx_full[s], 1);
+      // math, epilogue and MMA warps, the bias sums
+      mbar_init(&ctl->idx_empty[s], kMathWarps + 4 + 1 + (C::kSums ? 1 : 0));
     }
     mbar_init(&ctl->fix, 1);
     mbar_init(&ctl->a0_full, kKeys ? 1 : 4);
@@ -1124,6 +1196,8 @@ struct DCfg {
 struct DCtl {
   uint64_t full[kDqSlots], empty[kDqSlots], fix;
   uint64_t acc_full[2], acc_free[2];
+  uint64_t idx_full[kBwdIdxSlots], idx_empty[kBwdIdxSlots];
+  int idx_ring[kBwdIdxSlots];
   uint64_t drain;
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -1149,7 +1223,8 @@ __device__ void dq_load(const BwdParams& p, DCtl* ctl, uint8_t* smem, const Wait
                                           ((n_slot / kDqSlots) - 1) & 1u, w, kBSiteB0Empty);
   };
   for (int k = 0; ok; ++k) {
-    const int idx = bwd_item(k);
+    const int idx = bwd_claim(ctl, p.claims + 2, k, w);
+    if (idx == 0x7fffffff) ok = false;
     if (idx >= p.n_g) break;
     const BwdItem it = p.g_items[idx];
     const SeqRec sr = p.seqs[it.b];
@@ -1229,7 +1304,7 @@ __device__ void dq_mma(const BwdParams& p, DCtl* ctl, uint32_t tmem, const uint8
   uint32_t n_slot = 0, items = 0;
   bool ok = true;
   for (int k = 0; ok; ++k, ++items) {
-    const int idx = bwd_item(k);
+    const int idx = bwd_take(ctl, k, w);
     if (idx >= p.n_g) break;
     const BwdItem it = p.g_items[idx];
     const uint32_t buf = items & 1u;
@@ -1287,7 +1362,7 @@ __device__ void dq_epilogue(const BwdParams& p, DCtl* ctl, uint32_t tmem, const 
   const bool v8 = (reinterpret_cast<uintptr_t>(p.dq) & 31u) == 0;
   uint32_t items = 0;
   for (int k = 0;; ++k, ++items) {
-    const int idx = bwd_item(k);
+    const int idx = bwd_take(ctl, k, w);
     if (idx >= p.n_g) return;
     const BwdItem it = p.g_items[idx];
     const SeqRec sr = p.seqs[it.b];
@@ -1349,6 +1424,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_bwd_dq_sm100(const __grid_co
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->acc_full[s], 1);
       mbar_init(&ctl->acc_free[s], 8);
+    }
+    for (int s = 0; s < kBwdIdxSlots; ++s) {
+      mbar_init(&ctl->idx_full[s], 1);
+      mbar_init(&ctl->idx_empty[s], 9);  // epilogue and MMA warps
     }
     mbar_init(&ctl->fix, 1);
     mbar_init(&ctl->drain, 1);
