@@ -154,7 +154,14 @@ struct Cfg {
 template <int NS>
 struct Ctl {
   uint64_t q_full[2], q_empty[2];  // Q sub-tile s loaded / no longer read
-  uint64_t kv_full[NS], kv_empty[NS];
+  // Load r of the K/V ring goes to slot r % NS and completes kv_full[r % (2 NS)].
+  // A wait by parity holds only when the barrier's phase before it is over. K
+  // and V tiles are waited for by two threads and need not land in their order:
+  // with one barrier per slot and three slots, V(t) follows K(t) in its slot,
+  // and the thread that waits for V(t) may come before K(t) has landed. With
+  // two per slot the phase before a tile's is that of a tile this thread has
+  // waited for itself (or that left the slot before one it has waited for).
+  uint64_t kv_full[2 * NS], kv_empty[NS];
   uint64_t s_full[2];  // S_s in TMEM
   uint64_t s_free[2];  // S_s read into registers: the next QK_s may overwrite it
   uint64_t p_full[2];  // P_s in shared memory
@@ -407,11 +414,11 @@ __device__ void load_role(const FwdParams& p, Ctl<Cfg<D>::kStages>* ctl, uint8_t
         !wait_bounded(&ctl->kv_empty[st], ((ring / NS) - 1) & 1u, w, kSiteKvEmpty))
       return false;
     FA_STAMP(6, 1, ring);
-    mbar_expect_tx(&ctl->kv_full[st], C::kTileBytes);
+    uint64_t* full = &ctl->kv_full[ring % (2 * NS)];
+    mbar_expect_tx(full, C::kTileBytes);
 #pragma unroll
     for (int c = 0; c < C::kChunks; ++c)
-      tma_load_4d(sKV + st * C::kTileBytes + c * C::kChunkBytes, tm, &ctl->kv_full[st], c * 64,
-                  row, h, bc);
+      tma_load_4d(sKV + st * C::kTileBytes + c * C::kChunkBytes, tm, full, c * 64, row, h, bc);
     ++ring;
     return true;
   };
@@ -497,7 +504,7 @@ __device__ void load_role(const FwdParams& p, Ctl<Cfg<D>::kStages>* ctl, uint8_t
     // Abort: let every copy this thread started land before the CTA exits.
     const uint32_t first = ring > (uint32_t)NS ? ring - NS : 0u;
     for (uint32_t r = first; r < ring; ++r)
-      wait_bounded(&ctl->kv_full[r % NS], (r / NS) & 1u, w, kSiteDrain, false);
+      wait_bounded(&ctl->kv_full[r % (2 * NS)], (r / (2 * NS)) & 1u, w, kSiteDrain, false);
     for (int st = 0; st < 2; ++st)
       if (nq[st] > 0) wait_bounded(&ctl->q_full[st], (nq[st] - 1) & 1u, w, kSiteDrain, false);
   }
@@ -626,7 +633,7 @@ __device__ void qk_role(const FwdParams& p, Ctl<Cfg<D>::kStages>* ctl, uint32_t 
          t += kWalkStep<kRev>, ++g) {
       const uint32_t r = ring_k(g);
       FA_STAMP(2, 0, g);
-      if (!wait_bounded(&ctl->kv_full[r % NS], (r / NS) & 1u, w, kSiteKvFull)) {
+      if (!wait_bounded(&ctl->kv_full[r % (2 * NS)], (r / (2 * NS)) & 1u, w, kSiteKvFull)) {
         ok = false;
         break;
       }
@@ -705,7 +712,7 @@ __device__ void pv_role(const FwdParams& p, Ctl<Cfg<D>::kStages>* ctl, uint32_t 
       }
       const uint32_t r = ring_v(g, !have_next && last_t);
       FA_STAMP(3, 0, g);
-      if (!wait_bounded(&ctl->kv_full[r % NS], (r / NS) & 1u, w, kSiteKvFull)) {
+      if (!wait_bounded(&ctl->kv_full[r % (2 * NS)], (r / (2 * NS)) & 1u, w, kSiteKvFull)) {
         ok = false;
         break;
       }
@@ -1323,7 +1330,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_sm100(const __grid_constan
       mbar_init(&ctl->q_empty[s], 1);
     }
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&ctl->kv_full[s], 1);
+      mbar_init(&ctl->kv_full[2 * s], 1);
+      mbar_init(&ctl->kv_full[2 * s + 1], 1);
       mbar_init(&ctl->kv_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
