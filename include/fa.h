@@ -225,11 +225,13 @@ typedef struct {
  * The table is laid out by distance in the handle's workspace by a small
  * kernel ahead of the attention kernel, in every call (it is a weight that
  * changes between calls); the bucket map is uploaded when it differs from
- * the last call's. The other arguments and the asynchronous behaviour are
- * fa_fwd's. Errors: FA_ERR_NULLPTR (bias, table or bucket_of NULL),
- * FA_ERR_PARAM_INVALID (a bucket outside the table, reach or num_buckets
- * below 1, an unaligned table), FA_ERR_UNSUPPORTED on a stream that is being
- * captured into a graph, and fa_fwd's.
+ * the last call's. Sequences of one query row (or up to four, where the heads
+ * leave SMs idle) take a kernel that splits the keys over the SMs. The other
+ * arguments and the asynchronous behaviour are fa_fwd's. Errors:
+ * FA_ERR_NULLPTR (bias, table or bucket_of NULL), FA_ERR_PARAM_INVALID (a
+ * bucket outside the table, reach or num_buckets below 1, an unaligned table),
+ * FA_ERR_UNSUPPORTED on a stream that is being captured into a graph, and
+ * fa_fwd's.
  */
 fa_status_t fa_fwd_relbias(fa_handle_t h, const void* q, const void* k, const void* v,
                            const fa_relbias_t* bias, const int64_t* prefix,
@@ -252,16 +254,21 @@ fa_status_t fa_fwd_relbias(fa_handle_t h, const void* q, const void* k, const vo
  * dq, dk, dv   device bf16, shapes of q, k and v; every element is written.
  *              Rows that see no key get dq = 0 and add nothing to dk and dv,
  *              keys that no row sees get 0.
- * All device operands 16-byte aligned, lse and d_lse 4-byte. Operands of a
+ * All device operands 16-byte aligned, lse and d_lse 4-byte. The gradients may
+ * overlap neither an operand nor each other (FA_ERR_PARAM_INVALID). Operands of a
  * side without tokens (Sq or Skv 0) may be NULL.
  * P and dS are rounded to bf16 for the products that sum over them, as the
- * forward rounds P; all sums are fp32. Results are bitwise deterministic: dQ
- * and dK, dV come from two passes, each output row from one CTA in a fixed
- * order, at the price of recomputing the scores once more.
+ * forward rounds P; all sums are fp32. Results are bitwise deterministic: every
+ * sum has one fixed order, at the price of computing the scores twice, or of
+ * writing dS (bf16) to memory once: with D = 128 and more than 4 work items (128
+ * query rows or keys of a head) per SM.
  * The handle's work lists for the backward are kept beside the forward's, so
  * alternating the two rebuilds neither. Device workspace, grown on the first
- * calls: 1 KiB per 128 query rows and head, 64 bytes per 128 rows or keys and
- * head, and the pre-pass's tables for a dense mask.
+ * calls: 1 KiB per 128 query rows and head, about 130 bytes per 128 rows or
+ * keys and head, for a dense mask 2 bits per pair, and where dS is written 32
+ * KiB per pair of 128 rows and 128 keys that see each other, of the heads held
+ * at once: at most 4 GiB (a call whose single head needs more, or that cannot
+ * have the memory, computes the scores twice).
  * Errors: fa_fwd's, and FA_ERR_PARAM_INVALID for a handle that names an ALiBi
  * variant (fa_bwd_alibi), FA_ERR_UNSUPPORTED on a stream that is being
  * captured into a graph (the work lists would be another call's at replay).
@@ -286,10 +293,10 @@ fa_status_t fa_bwd_alibi(fa_handle_t h, const void* q, const void* k, const void
  * fa_bwd_relbias — fa_bwd after fa_fwd_relbias, with the bias's gradient
  *     dtable[c][h] = sum of dS over the visible pairs in bucket c.
  * dtable  device fp32 [num_buckets, N]; every element is written (0 for a
- *         bucket no pair falls in). Summed in fp32 in a fixed order.
+ *         bucket no pair falls in). Summed in fp32 or more in a fixed order.
  * The bias must be the forward's. Device workspace beside fa_bwd's:
- * 4 * (2 * reach + 1) bytes per 128 query rows and head. Errors as
- * fa_fwd_relbias and fa_bwd.
+ * 4 * (2 * reach + 513) bytes per 128 keys and head. Errors as fa_fwd_relbias
+ * and fa_bwd.
  */
 fa_status_t fa_bwd_relbias(fa_handle_t h, const void* q, const void* k, const void* v,
                            const fa_relbias_t* bias, const void* o, const float* lse,

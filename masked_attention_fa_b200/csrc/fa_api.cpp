@@ -87,18 +87,20 @@ fa_status_t bind_device(fa_handle_t h) {
                   h->device, dev);
     return FA_OK;
   }
-  cudaDeviceProp prop;
-  e = cudaGetDeviceProperties(&prop, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDeviceProperties");
-  if (prop.major != 10 || prop.minor != 0)
+  int major = 0, minor = 0, sms = 0;
+  e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+  if (major != 10 || minor != 0)
     return fail(FA_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library runs on sm_100 (B200)", dev,
-                prop.major, prop.minor);
+                major, minor);
   e = cudaEventCreateWithFlags(&h->stage_done, cudaEventDisableTiming);
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventCreate");
   e = cudaEventCreateWithFlags(&h->last_call, cudaEventDisableTiming);
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventCreate");
   h->device = dev;
-  h->num_sms = prop.multiProcessorCount;
+  h->num_sms = sms;
   return FA_OK;
 }
 
@@ -375,6 +377,7 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
     st = refuse_capture(stream);
     if (st != FA_OK) return st;
   }
+  FailedCall failed{h, stream, bias != nullptr};
   st = refresh_plan(h, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask, stream);
   if (st != FA_OK) return st;
   if (h->n_items == 0) return FA_OK;  // no query rows: nothing to write
@@ -384,6 +387,7 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
     const cudaError_t er = cudaEventRecord(h->last_call, stream);
     if (er != cudaSuccess) return cuda_fail(er, "cudaEventRecord");
     h->any_call = true;
+    failed.armed = false;
     return FA_OK;
   }
   st = encode_maps(h, q, k, v);
@@ -491,6 +495,7 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
   e = cudaEventRecord(h->last_call, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
   h->any_call = true;
+  failed.armed = false;
   return FA_OK;
 }
 

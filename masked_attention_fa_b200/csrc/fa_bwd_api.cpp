@@ -6,6 +6,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <exception>
+#include <iterator>
 #include <vector>
 
 #include "../../include/fa.h"
@@ -265,6 +266,35 @@ struct BwdArgs {
   float* dtable;
 };
 
+// A gradient written over an operand, or over another gradient, would be read
+// by the kernels beside its writer.
+bool outputs_apart(const fa_desc_t* d, const BwdArgs& a) {
+  const size_t seqs = d->layout == FA_TND ? 1 : (size_t)d->B, N = (size_t)d->N;
+  const size_t row_side = seqs * N * (size_t)d->Sq, key_side = seqs * N * (size_t)d->Skv,
+               D2 = (size_t)d->D * 2;
+  struct Range {
+    const void* at;
+    size_t bytes;
+  };
+  const size_t table = a.bias ? (size_t)a.bias->num_buckets * N * 4 : 0;
+  const size_t mask = (size_t)mask_planes(d, a.atten_mask != nullptr && d->sparse_mode <= 1) *
+                      (size_t)d->Sq * (size_t)d->Skv;
+  const Range ranges[] = {{a.dq, row_side * D2}, {a.dk, key_side * D2}, {a.dv, key_side * D2},
+                          {a.dtable, table},     {a.q, row_side * D2},  {a.k, key_side * D2},
+                          {a.v, key_side * D2},  {a.o, row_side * D2},  {a.d_o, row_side * D2},
+                          {a.lse, row_side * 4}, {a.d_lse, row_side * 4},
+                          {a.slopes, N * 4},     {a.bias ? a.bias->table : nullptr, table},
+                          {a.atten_mask, mask}};
+  constexpr int kOutputs = 4;
+  for (int i = 0; i < kOutputs; ++i)
+    for (const Range* r = ranges + i + 1; r != std::end(ranges); ++r) {
+      const uintptr_t x = (uintptr_t)ranges[i].at, y = (uintptr_t)r->at;
+      if (x && y && r->bytes && ranges[i].bytes && x < y + r->bytes && y < x + ranges[i].bytes)
+        return false;
+    }
+  return true;
+}
+
 fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream) {
   const fa_desc_t* d = &h->desc;
   const bool rows = d->Sq > 0, keys = d->Skv > 0;
@@ -281,6 +311,8 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
     return fail(FA_ERR_PARAM_INVALID, "q, k, v, o, d_o, dq, dk and dv must be 16-byte aligned");
   if (((uintptr_t)a.lse | (uintptr_t)a.d_lse | (uintptr_t)a.slopes | (uintptr_t)a.dtable) & 3u)
     return fail(FA_ERR_PARAM_INVALID, "lse, d_lse, slopes and dtable must be 4-byte aligned");
+  if (!outputs_apart(d, a))
+    return fail(FA_ERR_PARAM_INVALID, "a gradient overlaps an operand or another gradient");
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   st = refuse_capture(stream);
   if (st != FA_OK) return st;
@@ -293,6 +325,7 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
     e = cudaStreamWaitEvent(stream, h->last_call, 0);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
   }
+  FailedCall failed{h, stream, true};
   st = refresh_lists(h, a.prefix, a.cu_q, a.cu_kv, has_mask, stream);
   if (st != FA_OK) return st;
   int64_t ds_tiles = 0;
@@ -455,6 +488,7 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   e = cudaEventRecord(h->last_call, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
   h->any_call = true;
+  failed.armed = false;
   return FA_OK;
 }
 

@@ -96,6 +96,16 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 bool env_flag(const char* name);
 fa_status_t cuda_fail(cudaError_t e, const char* what);
+// Orders the handle's later calls after a call that fails half-way: what it
+// has uploaded until then may still be on its way, and counts as uploaded.
+struct FailedCall {
+  fa_handle_t h;
+  cudaStream_t stream;
+  bool armed;
+  ~FailedCall() {
+    if (armed && cudaEventRecord(h->last_call, stream) == cudaSuccess) h->any_call = true;
+  }
+};
 // Binds the handle to the current device at its first call and refuses
 // calls with another device current.
 fa_status_t bind_device(fa_handle_t h);
