@@ -1,36 +1,53 @@
-// Masked attention backward for B200 (sm_100a), two kernels of one structure.
+// Masked attention backward for B200 (sm_100a).
 //
 // With P = exp(score - lse) over the visible pairs and delta = sum dO o (see
 // fa_bwd.h for the row statistics):
 //     dV = P^T dO,   dS = P * (dO V^T - delta),   dQ = scale dS K,
 //     dK = scale dS^T Q
-// Neither P nor dS is written out: the query walk (kKeys = false) holds 128
-// query rows and visits their key tiles for dQ, the key walk (kKeys = true)
-// holds 128 keys and visits their query tiles for dK and dV. Each recomputes
-// the scores, so seven products run instead of five; in return every sum
-// stays in tensor memory and has one fixed order: no partial gradients go
-// through L2, no atomics, equal bits on every call.
+//
+// Two walks, one structure. The query walk (kKeys = false) holds 128 query rows
+// and visits their key tiles for dQ, the key walk (kKeys = true) holds 128 keys
+// and visits their query tiles for dK and dV. Each recomputes the scores: seven
+// products a pair of tiles, but every sum stays in tensor memory and has one
+// fixed order: no partial gradients go through L2, no atomics, equal bits on
+// every call. Or the key walk writes dS out once and a third kernel
+// (fa_bwd_dq_sm100) multiplies it by K: five products and 32 KB written and
+// read a pair of tiles. Adding the key tiles' shares of dQ up in L2 instead was
+// built and measured: red.add of 64 KB a step runs at about 2.6 TB/s over the
+// card, 3,200 cycles a step (causal 2 x 16 x 4096 x 128: 444 us against 394).
 //
 // The walks are the same chain with the roles of the operands exchanged. A0,
 // A1 are held (Q, dO; K, V) and B0, B1 streamed (K, V; Q, dO):
 //     S = A0 B0^T, dP = A1 B1^T, acc0 += dS B0 (dQ; dK), acc1 += P B1 (dV)
 // The rows of every product are tensor memory lanes, and P and dS go back to
 // tensor memory in bf16, over the scores they came from, as the A operand of
-// the accumulating products: shared memory only feeds B (and, in the key
-// walk at head dim 128, where tensor memory is full, A0 and A1).
+// the accumulating products, so that shared memory feeds only their B; the
+// query walk also holds A0 and A1 in tensor memory (the key walk at head dim
+// 128 has no room left there).
 //
-// One persistent CTA per SM, 16 warps:
-//   warps 0-7   P and dS; warps 0-3 columns 0..63 of a tile, 4-7 64..127
-//   warps 8-11  epilogue: accumulators to global memory; query walk: Q and
-//               dO of the next item from global to tensor memory
-//   warp 12     all MMAs (one lane issues; owns tensor memory)
-//   warp 13     TMA loads; clears the rows of a streamed tile that belong to
-//               the next packed sequence
-//   warp 14     idle
-//   warp 15     bias gradient: the tile's sums by distance (query walk)
-// MMA order per step: query walk S(t+1), dQ(t), dP(t+1); key walk dV(i),
-// S(i+1), dK(i), dP(i+1), also across items, so that the products of one
-// step run while P and dS of the other are computed.
+// One persistent CTA per SM, 24 warps:
+//   warps 0-15   P and dS, four groups of four warps, 32 columns of a tile each
+//   warps 16-19  epilogue: accumulators to global memory; query walk: Q and
+//                dO of the next item from global to tensor memory
+//   warp 20      all products (one lane issues; owns tensor memory)
+//   warp 21      TMA loads; claims the items; clears the rows of a streamed
+//                tile that belong to the next packed sequence
+//   warp 22      idle
+//   warp 23      bias gradient: the tile's sums by distance (key walk)
+// Order of the products: query walk S(t+1), dQ(t), dP(t+1); key walk dV(i),
+// S(i+1), dK(i), dP(i+1), also across items, so that the products of one step
+// run while P and dS of the other are computed. They are issued by an elected
+// lane of a converged warp, which keeps descriptors in uniform registers: a
+// thread of its own took 560 to 1,400 cycles to issue eight products, this 410
+// to 520, their execution.
+//
+// What bounds it. Head dim 128: the card's power limit (1,000 W, about 1.45
+// GHz, on anything longer than a few milliseconds; the products' rate is then
+// 0.84 of what cuBLAS sustains there), so products and bytes count, not
+// cycles: an exponential on the FMA pipe, stores moved to other warps or a
+// shorter chain cost or change nothing. Head dim 64: the math warps, whose
+// phases (scores to P, dP to dS) follow each other; the issue slots are 56 %
+// busy, the MUFU unit 40 %.
 // Every mbarrier wait is bounded, as in the forward.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -816,7 +833,9 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
           }
           // 8 columns of a warp's rows are 512 contiguous bytes. (Rows of the
           // whole tile are 32 lines a store, which keep shared memory from the
-          // products: key walk 252 us against 234 on a causal 2 x 16 x 4096 x 128.)
+          // products: key walk 252 us against 234 on a causal 2 x 16 x 4096 x 128.
+          // The stores still take 900 of a step's 3,800 cycles; written by the
+          // epilogue from tensor memory instead, the call was 3 % slower.)
           __nv_bfloat16* dst = ds_out + (int64_t)t * (128 * 128);
 #pragma unroll
           for (int u = 0; u < kCols / 8; ++u)
@@ -825,10 +844,7 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
         }
       }
       if constexpr (kGrad) {
-        if (!stored) {
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) x[c] = 0.f;
-        }
+        // (Rows past the sequence's end do not count, whatever they hold.)
         if (near) {
           // Sums by diagonal of this warp's 32 rows x kCols columns: the running
           // sum of a diagonal moves to the next lane with each column, and
@@ -844,7 +860,7 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
             const float up = __shfl_up_sync(0xffffffffu, s, 1);
-            s = (lane == 0 ? 0.f : up) + x[c];
+            s = (lane == 0 ? 0.f : up) + (stored ? x[c] : 0.f);
             if (lane == 31) out[c] = s;
           }
           if (lane < 31) out[kCols + 30 - lane] = s;
@@ -859,8 +875,10 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
             add_x2(acc[2], acc[3], x[c + 2], x[c + 3]);
           }
           const float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          if (rel0 < 0) far_lo += s;
-          else far_hi += s;
+          if (stored) {
+            if (rel0 < 0) far_lo += s;
+            else far_hi += s;
+          }
         }
       }
     }
