@@ -112,17 +112,17 @@ int64_t spill_tiles() {
   return (int64_t(4) << 30) / (128 * 128 * 2);
 }
 
-// Items without a tile first (their zeros are written beside the first items'
-// products), then longest first, in buckets of similar length inside which the
-// items of one (sequence, head) stand together: the tiles in flight then share
-// their operands through L2 (see order_work_list). The kernels claim them in
-// this order.
+// Longest first, in buckets of similar length inside which the items of one
+// (sequence, head) stand together: the tiles in flight then share their
+// operands through L2 (see order_work_list). The kernels claim them in this
+// order; the last, without a tile, are zeros to write, which fill the end of
+// the SMs that are done (164 us on a band 2 x 8k of 32 heads, 167 with them in
+// front, 170 with them spread).
 void order_items(std::vector<BwdItem>::iterator first, std::vector<BwdItem>::iterator last,
                  int num_sms) {
   const int32_t bucket = claims_items(last - first, num_sms) ? kLocalityTiles : 1;
   std::sort(first, last, [bucket](const BwdItem& a, const BwdItem& c) {
-    const int32_t la = a.hi - a.lo, lc = c.hi - c.lo;
-    if ((la <= 0) != (lc <= 0)) return la <= 0;
+    const int32_t la = std::max(a.hi - a.lo, 0), lc = std::max(c.hi - c.lo, 0);
     const int32_t ba = (la + bucket - 1) / bucket, bc = (lc + bucket - 1) / bucket;
     if (ba != bc) return ba > bc;
     if (a.b != c.b) return a.b < c.b;

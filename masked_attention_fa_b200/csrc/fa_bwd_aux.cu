@@ -97,7 +97,7 @@ __device__ __forceinline__ void mask_tile(const BwdMaskParams& a, int64_t tile) 
 }
 
 // One CTA per query tile, D / 8 threads per row (16-byte loads, whole rows
-// per group of threads): delta_i = sum_d do_id o_id.
+// per group of threads): delta_i = sum_d do_id o_id. Bound by memory.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_stats(const __grid_constant__ BwdParams p,
                                                  const __grid_constant__ BwdMaskParams a,
@@ -124,38 +124,43 @@ __global__ void __launch_bounds__(256) bwd_stats(const __grid_constant__ BwdPara
   const SeqRec s = p.seqs[it.b];
   const int sl = threadIdx.x % L;
   const int64_t base = it.b * p.q_sb + it.h * p.q_sh;
-  float* out = p.stats + (int64_t)it.stat * 256;
+  const int row = threadIdx.x;  // of the first 128 threads
+  const int64_t i0 = (int64_t)it.tile * kTileM;
+  const bool stored = row < kTileM && i0 + row < s.sq;
+  const int64_t at = it.b * p.l_sb + it.h * p.l_sh + s.q_off + i0 + row;
+  float l = stored ? p.lse[at] : -INFINITY;
+  const float dl = stored && p.d_lse ? p.d_lse[at] : 0.f;
+  // Addresses are kept inside the sequence, so that all loads are in flight.
+  uint4 vo[kTileM / R], vd[kTileM / R];
 #pragma unroll
-  for (int r0 = 0; r0 < kTileM; r0 += R) {
-    const int r = r0 + threadIdx.x / L;
-    const int64_t i = (int64_t)it.tile * kTileM + r;
-    const bool stored = i < s.sq;
-    float d = 0.f;
-    if (stored) {
-      const int64_t off = base + (s.q_off + i) * p.q_st + sl * 8;
-      d = dot8(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.o) + off)),
-               __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.d_o) + off)));
-    }
-#pragma unroll
-    for (int x = 1; x < L; x <<= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-    if (sl == 0) {
-      float nl = -INFINITY, nd = 0.f;
-      if (stored) {
-        const int64_t at = it.b * p.l_sb + it.h * p.l_sh + s.q_off + i;
-        float l = p.lse[at];
-        if (l != -INFINITY) {
-          // Left-aligned ALiBi: the same weights as the right-aligned bias,
-          // which the kernels add, with every score of the row shifted.
-          if (p.alibi == FA_ALIBI_LEFT)
-            l = fmaf(-p.slopes[it.h], (float)(i + (int64_t)s.skv - s.sq), l);
-          nl = -l * kLog2e;
-          nd = (p.d_lse ? p.d_lse[at] : 0.f) - d;
-        }
-      }
-      out[r] = nl;
-      out[kTileM + r] = nd;
-    }
+  for (int x = 0; x < kTileM / R; ++x) {
+    const int64_t i = imin64(i0 + x * R + threadIdx.x / L, s.sq - 1);
+    const int64_t off = base + (s.q_off + i) * p.q_st + sl * 8;
+    vo[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.o) + off));
+    vd[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.d_o) + off));
   }
+  __shared__ float delta[kTileM];
+#pragma unroll
+  for (int x = 0; x < kTileM / R; ++x) {
+    float d = dot8(vo[x], vd[x]);
+#pragma unroll
+    for (int y = 1; y < L; y <<= 1) d += __shfl_xor_sync(0xffffffffu, d, y);
+    if (sl == 0) delta[x * R + threadIdx.x / L] = d;
+  }
+  __syncthreads();
+  if (row >= kTileM) return;
+  float nl = -INFINITY, nd = 0.f;
+  if (l != -INFINITY) {
+    // Left-aligned ALiBi: the same weights as the right-aligned bias, which
+    // the kernels add, with every score of the row shifted.
+    if (p.alibi == FA_ALIBI_LEFT)
+      l = fmaf(-p.slopes[it.h], (float)(i0 + row + (int64_t)s.skv - s.sq), l);
+    nl = -l * kLog2e;
+    nd = dl - delta[row];
+  }
+  float* out = p.stats + (int64_t)it.stat * 256;
+  out[row] = nl;
+  out[kTileM + row] = nd;
 }
 
 // [lo, hi) and the longest run of FULL (the first on ties) of n classes
