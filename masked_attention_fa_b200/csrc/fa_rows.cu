@@ -228,10 +228,13 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) rows_forward(const RowsPara
   };
   auto put = [&](int r, int d, float acc, float mm, float ll) {
     __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + q_off + r * p.q_st;
-    dst[d] = __float2bfloat16_rn(ll > 0.f ? acc / ll : 0.f);
+    // A row that sees nothing has the sum 0; a NaN score makes it NaN, which
+    // o and lse keep.
+    const bool none = ll == 0.f;
+    dst[d] = __float2bfloat16_rn(none ? 0.f : acc / ll);
     if (d == 0)
       p.lse[b * p.l_sb + h * p.l_sh + sr.q_off + r] =
-          ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+          none ? -INFINITY : (mm + log2f(ll)) * kLn2;
   };
   for (int x = threadIdx.x; x < rows * D; x += 32 * kWarps) {
     const int r = x / D, d = x % D;
