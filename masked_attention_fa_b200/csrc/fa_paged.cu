@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(128) paged_merge(const PagedParams p) {
 #pragma unroll
   for (int x = 0; x < D / 32; ++x) orow[lane + 32 * x] = __float2bfloat16_rn(acc[x] * inv);
   if (lane == 0)
-    p.lse[(int64_t)g.h * p.t_q + t] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+    // The sum is 0 only where no key is visible; a NaN score makes it, and lse, NaN.
+    p.lse[(int64_t)g.h * p.t_q + t] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
 template <int D>
