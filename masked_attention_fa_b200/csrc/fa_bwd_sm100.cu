@@ -158,10 +158,12 @@ __device__ __forceinline__ void mul_x2(float& a, float& b, float x, float y) {
 }
 
 // 2^x for two values on the FMA pipe: x = n + f with n = floor(x) (adding
-// 1.5 * 2^23 rounded down leaves n in the low mantissa bits), a polynomial of
-// degree kDeg for 2^f on [0, 1) and n added into the exponent field. p(0) = 1
-// exactly, so that x <= -127 (a masked pair) gives 0. Relative error 3.0e-6
-// (degree 4) and 1.6e-7 (degree 5); coefficients from gen_exp2_poly.py.
+// 1.5 * 2^23 rounded down leaves n in the low mantissa bits), a polynomial p of
+// degree kDeg for 2^f on [0, 1), p(f) = 1 + f r(f), as 2^n + (2^n f) r(f) with the
+// float 2^n whose exponent field is n + 127: exact, 0 for x < -126 (a masked
+// pair) and NaN for NaN (n added into p's exponent field instead would carry
+// NaN into a finite value). Relative error 3.0e-6 (degree 4) and 1.6e-7 (degree 5); coefficients from
+// gen_exp2_poly.py.
 template <int kDeg>
 __device__ __forceinline__ void ex2_floor_x2(float& a, float& b) {
   static_assert(kDeg == 4 || kDeg == 5, "fitted degrees");
@@ -185,10 +187,16 @@ __device__ __forceinline__ void ex2_floor_x2(float& a, float& b) {
   const uint64_t f2 = pack_f32x2(fa, fb);
   float pa = kC[kDeg - 4][kDeg], pb = pa;
 #pragma unroll
-  for (int i = kDeg - 1; i >= 0; --i)
+  for (int i = kDeg - 1; i > 0; --i)
     fma_x2(pa, pb, f2, pack_f32x2(kC[kDeg - 4][i], kC[kDeg - 4][i]));
-  a = __int_as_float(__float_as_int(pa) + (__float_as_int(ta) << 23));
-  b = __int_as_float(__float_as_int(pb) + (__float_as_int(tb) << 23));
+  // 2^n: the low 9 bits of 1.5 * 2^23 are 0, only n is left of t's bits.
+  const float na = __int_as_float((__float_as_int(ta) << 23) + 0x3f800000);
+  const float nb = __int_as_float((__float_as_int(tb) << 23) + 0x3f800000);
+  static_assert(kC[kDeg - 4][0] == 1.0f, "2^n stands for 2^n kC[0]");
+  mul_x2(fa, fb, na, nb);
+  fma_x2(pa, pb, pack_f32x2(fa, fb), pack_f32x2(na, nb));
+  a = pa;
+  b = pb;
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
