@@ -90,11 +90,16 @@ fa_status_t prepare_rel(fa_handle_t h, const fa_relbias_t* bias, cudaStream_t st
     held.clear();
     st = ensure_buffer(h, &h->rel.map, entries * sizeof(int32_t));
     if (st != FA_OK) return st;
-    // Pageable memory: the call returns once the source has been read.
-    const cudaError_t e = cudaMemcpyAsync(h->rel.map.ptr, bias->bucket_of,
-                                          entries * sizeof(int32_t), cudaMemcpyHostToDevice, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyAsync(bucket map)");
+    // From the handle's own copy, which is pageable: the call returns once it
+    // has been read. (The caller's map may be pinned memory, which the copy
+    // would read later, when the caller has rewritten it.)
     held.assign(bias->bucket_of, bias->bucket_of + entries);
+    const cudaError_t e = cudaMemcpyAsync(h->rel.map.ptr, held.data(), entries * sizeof(int32_t),
+                                          cudaMemcpyHostToDevice, stream);
+    if (e != cudaSuccess) {
+      held.clear();
+      return cuda_fail(e, "cudaMemcpyAsync(bucket map)");
+    }
   }
   float* ext = static_cast<float*>(h->rel.ext.ptr);
   *out = RelBias{ext, R, row};
