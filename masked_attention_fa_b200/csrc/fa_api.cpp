@@ -106,16 +106,19 @@ fa_status_t bind_device(fa_handle_t h) {
 
 
 // Make sure the device workspace holds `bytes`; the error word is zeroed
-// whenever the workspace is (re)allocated.
+// whenever the workspace is (re)allocated. The plan in the old one goes with
+// it, also when there is no memory for a new one: a later call that finds its
+// lengths in the plan's key would run on a workspace without its list.
 fa_status_t ensure_workspace(fa_handle_t h, size_t bytes) {
   if (h->d_ws != nullptr && h->ws_bytes >= bytes) return FA_OK;
-  if (env_flag("FA_TEST_FAIL_ALLOC")) return fail(FA_ERR_ALLOC, "device workspace (test hook)");
   if (h->d_ws != nullptr) {
     if (h->any_call) cudaEventSynchronize(h->last_call);
     cudaFree(h->d_ws);
     h->d_ws = nullptr;
     h->ws_bytes = 0;
   }
+  h->plan_valid = false;
+  if (env_flag("FA_TEST_FAIL_ALLOC")) return fail(FA_ERR_ALLOC, "device workspace (test hook)");
   size_t want = align_up(bytes < 4096 ? 4096 : bytes, 4096);
   cudaError_t e = cudaMalloc(&h->d_ws, want);
   if (e != cudaSuccess) {
@@ -218,6 +221,7 @@ fa_status_t refresh_plan(fa_handle_t h, const int64_t* prefix, const int64_t* cu
       }
     }
   }
+  h->plan_valid = false;  // until the new one is whole
   e = cudaMemcpyAsync(static_cast<uint8_t*>(h->d_ws) + kHeaderBytes, hs, payload,
                       cudaMemcpyHostToDevice, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyAsync(work list)");
@@ -610,6 +614,7 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
     if (!groups.empty()) std::memcpy(hs + seq_bytes, groups.data(), groups.size() * sizeof(PagedGroup));
     if (!units.empty())
       std::memcpy(hs + seq_bytes + group_bytes, units.data(), units.size() * sizeof(PagedUnit));
+    h->plan_valid = false;
     e = cudaMemcpyAsync(static_cast<uint8_t*>(h->d_ws) + kHeaderBytes, hs, payload,
                         cudaMemcpyHostToDevice, stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyAsync(paged work list)");
@@ -708,6 +713,7 @@ fa_status_t fa_sync_status(fa_handle_t h) {
   if (!h->any_call) return FA_OK;
   cudaError_t e = cudaEventSynchronize(h->last_call);
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventSynchronize");
+  if (h->d_ws == nullptr) return FA_OK;  // a call since then found no memory
   unsigned int word = 0;
   e = cudaMemcpy(&word, h->d_ws, sizeof(word), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(error word)");
