@@ -109,7 +109,10 @@ fa_status_t bind_device(fa_handle_t h) {
 // whenever the workspace is (re)allocated. The plan in the old one goes with
 // it, also when there is no memory for a new one: a later call that finds its
 // lengths in the plan's key would run on a workspace without its list.
-fa_status_t ensure_workspace(fa_handle_t h, size_t bytes) {
+// The header is cleared on the call's stream: on the default stream it could
+// wait behind other work there while the call's kernels, on a stream that does
+// not wait for that one, already read the claim counters.
+fa_status_t ensure_workspace(fa_handle_t h, size_t bytes, cudaStream_t stream) {
   if (h->d_ws != nullptr && h->ws_bytes >= bytes) return FA_OK;
   if (h->d_ws != nullptr) {
     if (h->any_call) cudaEventSynchronize(h->last_call);
@@ -125,8 +128,8 @@ fa_status_t ensure_workspace(fa_handle_t h, size_t bytes) {
     h->d_ws = nullptr;
     return fail(FA_ERR_ALLOC, "cudaMalloc(%zu): %s", want, cudaGetErrorString(e));
   }
-  e = cudaMemset(h->d_ws, 0, kHeaderBytes);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemset");
+  e = cudaMemsetAsync(h->d_ws, 0, kHeaderBytes, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
   h->ws_bytes = want;
   return FA_OK;
 }
@@ -198,7 +201,8 @@ fa_status_t refresh_plan(fa_handle_t h, const int64_t* prefix, const int64_t* cu
   const size_t occ = planes ? occupancy_bytes(planes, h->desc.Sq, h->desc.Skv) : 0;
   fa_status_t st = ensure_workspace(
       h, planes ? occupancy_offset((int32_t)recs.size(), (int32_t)items.size()) + occ
-                : kHeaderBytes + payload);
+                : kHeaderBytes + payload,
+      stream);
   if (st != FA_OK) return st;
   st = ensure_stage(h, payload);
   if (st != FA_OK) return st;
@@ -381,7 +385,7 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
     st = refuse_capture(stream);
     if (st != FA_OK) return st;
   }
-  FailedCall failed{h, stream, bias != nullptr};
+  FailedCall failed{h, stream, true};
   st = refresh_plan(h, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask, stream);
   if (st != FA_OK) return st;
   if (h->n_items == 0) return FA_OK;  // no query rows: nothing to write
@@ -580,6 +584,7 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
   st = bind_device(h);
   if (st != FA_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  FailedCall failed{h, stream, true};
   const int64_t D = d->D;
   std::vector<int64_t> key = {-2, block_size, max_blocks};
   key.insert(key.end(), actual_seq_qlen, actual_seq_qlen + d->B);
@@ -599,7 +604,8 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
     const size_t seq_bytes = align_up(recs.size() * sizeof(SeqRec), 256);
     const size_t group_bytes = align_up(groups.size() * sizeof(PagedGroup), 256);
     const size_t payload = seq_bytes + group_bytes + units.size() * sizeof(PagedUnit);
-    st = ensure_workspace(h, align_up(kHeaderBytes + payload, 256) + units.size() * part_unit);
+    st = ensure_workspace(h, align_up(kHeaderBytes + payload, 256) + units.size() * part_unit,
+                          stream);
     if (st != FA_OK) return st;
     st = ensure_stage(h, payload);
     if (st != FA_OK) return st;
@@ -669,6 +675,7 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
   e = cudaEventRecord(h->last_call, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
   h->any_call = true;
+  failed.armed = false;
   return FA_OK;
 }
 
@@ -721,6 +728,7 @@ fa_status_t fa_sync_status(fa_handle_t h) {
   // Clear the whole header: the error word and, should an aborted launch
   // have left them set, the claim counters.
   e = cudaMemset(h->d_ws, 0, kHeaderBytes);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // the next call may not wait for it
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(header)");
   if (word & kErrTimeout)
     return fail(FA_ERR_TIMEOUT, "a device-side wait gave up (site %u); outputs are undefined",

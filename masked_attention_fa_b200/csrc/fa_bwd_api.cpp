@@ -323,7 +323,7 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   if (st != FA_OK) return st;
   st = bind_device(h);
   if (st != FA_OK) return st;
-  st = ensure_workspace(h, kHeaderBytes);  // the error word
+  st = ensure_workspace(h, kHeaderBytes, stream);  // the error word
   if (st != FA_OK) return st;
   cudaError_t e = cudaSuccess;
   if (h->any_call) {  // lists and scratch are rewritten: order after the last call

@@ -109,7 +109,7 @@ struct FailedCall {
 // Binds the handle to the current device at its first call and refuses
 // calls with another device current.
 fa_status_t bind_device(fa_handle_t h);
-fa_status_t ensure_workspace(fa_handle_t h, size_t bytes);
+fa_status_t ensure_workspace(fa_handle_t h, size_t bytes, cudaStream_t stream);
 // Grows a buffer to `bytes` (waiting for the handle's last call before the
 // old one is freed); its contents are lost.
 fa_status_t ensure_buffer(fa_handle_t h, DeviceBuffer* buf, size_t bytes);
