@@ -168,6 +168,14 @@ fa_status_t fa_create(const fa_desc_t* desc, fa_handle_t* out);
  * CTA takes a fixed share. Every output row is produced by one CTA either
  * way, so results do not depend on which CTA computed them.
  *
+ * Graphs: fa_fwd, fa_fwd_alibi, fa_fwd_with_ranges and fa_fwd_paged can be
+ * captured into a CUDA graph once the handle holds the work list of these
+ * lengths (make the call once outside the capture; FA_ERR_UNSUPPORTED
+ * otherwise). Replays use that list and its workspace, which the handle keeps
+ * until fa_destroy, beside a new one when a later call has other lengths. The
+ * rule on overlapping calls holds for replays too, and the handle does not
+ * wait for them: synchronise their stream before fa_sync_status or fa_destroy.
+ *
  * Asynchronous: returns once the kernel is enqueued. The host arrays are
  * read during the call only. Device-side problems (a wait that gave up) are
  * reported by fa_sync_status. The device must be sm_100 (B200 class);

@@ -105,6 +105,41 @@ fa_status_t bind_device(fa_handle_t h) {
 }
 
 
+fa_status_t stream_capturing(cudaStream_t stream, bool* capturing) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  *capturing = cap != cudaStreamCaptureStatusNone;
+  return FA_OK;
+}
+
+fa_status_t order_after_last(fa_handle_t h, bool capturing, cudaStream_t stream) {
+  if (!h->any_call || capturing) return FA_OK;
+  const cudaError_t e = cudaStreamWaitEvent(stream, h->last_call, 0);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "cudaStreamWaitEvent");
+}
+
+fa_status_t record_call(fa_handle_t h, bool capturing, cudaStream_t stream) {
+  if (capturing) {
+    h->captured = true;
+    return FA_OK;
+  }
+  const cudaError_t e = cudaEventRecord(h->last_call, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
+  h->any_call = true;
+  return FA_OK;
+}
+
+// The graph of a captured call reads the workspace's list at every replay: a
+// new list goes into a new workspace, and the old one is kept.
+void retire_captured(fa_handle_t h) {
+  if (!h->captured) return;
+  h->retired.push_back(h->d_ws);
+  h->d_ws = nullptr;
+  h->ws_bytes = 0;
+  h->captured = false;
+}
+
 // Make sure the device workspace holds `bytes`; the error word is zeroed
 // whenever the workspace is (re)allocated. The plan in the old one goes with
 // it, also when there is no memory for a new one: a later call that finds its
@@ -176,10 +211,18 @@ std::vector<int64_t> make_key(const fa_desc_t* d, const int64_t* prefix, const i
 
 namespace {
 
+// A captured upload would read the staging memory of a later call at replay.
+fa_status_t no_plan_in_capture() {
+  return fail(FA_ERR_UNSUPPORTED,
+              "these lengths need a new work list, which cannot be captured: make the call once "
+              "outside the capture first");
+}
+
 fa_status_t refresh_plan(fa_handle_t h, const int64_t* prefix, const int64_t* cu_q,
-                         const int64_t* cu_kv, int has_mask, cudaStream_t stream) {
+                         const int64_t* cu_kv, int has_mask, bool capturing, cudaStream_t stream) {
   std::vector<int64_t> key = make_key(&h->desc, prefix, cu_q, cu_kv, has_mask);
   if (h->plan_valid && key == h->plan_key) return FA_OK;
+  if (capturing) return no_plan_in_capture();
   std::vector<SeqRec> recs = decode_geometry(&h->desc, prefix, cu_q, cu_kv, has_mask);
   std::vector<WorkItem> items = build_items(&h->desc, recs);
   if (items.size() > (size_t)0x7fffffff) return fail(FA_ERR_UNSUPPORTED, "too many work items");
@@ -199,6 +242,7 @@ fa_status_t refresh_plan(fa_handle_t h, const int64_t* prefix, const int64_t* cu
   const size_t payload = planes ? align_up(seq_bytes, 256) + item_bytes
                                 : tr_off - kHeaderBytes + tr_bytes;
   const size_t occ = planes ? occupancy_bytes(planes, h->desc.Sq, h->desc.Skv) : 0;
+  retire_captured(h);
   fa_status_t st = ensure_workspace(
       h, planes ? occupancy_offset((int32_t)recs.size(), (int32_t)items.size()) + occ
                 : kHeaderBytes + payload,
@@ -208,10 +252,9 @@ fa_status_t refresh_plan(fa_handle_t h, const int64_t* prefix, const int64_t* cu
   if (st != FA_OK) return st;
   cudaError_t e = cudaEventSynchronize(h->stage_done);  // previous upload has left staging
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventSynchronize");
-  if (h->any_call) {  // a kernel of this handle on another stream may still read the old list
-    e = cudaStreamWaitEvent(stream, h->last_call, 0);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
-  }
+  // A kernel of this handle on another stream may still read the old list.
+  st = order_after_last(h, false, stream);
+  if (st != FA_OK) return st;
   uint8_t* hs = static_cast<uint8_t*>(h->h_stage);
   std::memcpy(hs, recs.data(), seq_bytes);
   if (item_bytes) std::memcpy(hs + align_up(seq_bytes, 256), items.data(), item_bytes);
@@ -381,22 +424,18 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
   st = bind_device(h);
   if (st != FA_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  if (bias) {
-    st = refuse_capture(stream);
-    if (st != FA_OK) return st;
-  }
-  FailedCall failed{h, stream, true};
-  st = refresh_plan(h, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask, stream);
+  bool capturing = false;
+  st = bias ? refuse_capture(stream) : stream_capturing(stream, &capturing);
+  if (st != FA_OK) return st;
+  FailedCall failed{h, stream, !capturing};
+  st = refresh_plan(h, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask, capturing, stream);
   if (st != FA_OK) return st;
   if (h->n_items == 0) return FA_OK;  // no query rows: nothing to write
   if (bias && few_rows(h->max_rows, d->B * d->N, h->num_sms)) {
     st = forward_rows(h, q, k, v, bias, o, lse, stream);
     if (st != FA_OK) return st;
-    const cudaError_t er = cudaEventRecord(h->last_call, stream);
-    if (er != cudaSuccess) return cuda_fail(er, "cudaEventRecord");
-    h->any_call = true;
     failed.armed = false;
-    return FA_OK;
+    return record_call(h, capturing, stream);
   }
   st = encode_maps(h, q, k, v);
   if (st != FA_OK) return st;
@@ -446,10 +485,8 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
                   h->n_items, (long long)sp.B * sp.N * sp.nblk);
     // The list, item_tr and the pre-pass's table are rewritten every call:
     // a kernel of this handle on another stream may still be reading them.
-    if (h->any_call) {
-      cudaError_t e = cudaStreamWaitEvent(stream, h->last_call, 0);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
-    }
+    st = order_after_last(h, capturing, stream);
+    if (st != FA_OK) return st;
     if (ranges != nullptr) {
       a.ranges = reinterpret_cast<TileRange*>(const_cast<int32_t*>(ranges));
     } else {
@@ -500,11 +537,8 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
     if (why) return fail(FA_ERR_UNSUPPORTED, "launch refused: %s", why);
     return cuda_fail(e, "kernel launch");
   }
-  e = cudaEventRecord(h->last_call, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
-  h->any_call = true;
   failed.armed = false;
-  return FA_OK;
+  return record_call(h, capturing, stream);
 }
 
 }  // namespace
@@ -584,7 +618,10 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
   st = bind_device(h);
   if (st != FA_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  FailedCall failed{h, stream, true};
+  bool capturing = false;
+  st = stream_capturing(stream, &capturing);
+  if (st != FA_OK) return st;
+  FailedCall failed{h, stream, !capturing};
   const int64_t D = d->D;
   std::vector<int64_t> key = {-2, block_size, max_blocks};
   key.insert(key.end(), actual_seq_qlen, actual_seq_qlen + d->B);
@@ -593,6 +630,7 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
   const int32_t hpu = paged_heads_per_unit(d->N, (int)D);
   const size_t part_unit = (size_t)hpu * kPagedRows * (size_t)(D + 4) * sizeof(float);
   if (!h->plan_valid || key != h->plan_key) {
+    if (capturing) return no_plan_in_capture();
     std::vector<SeqRec> recs = decode_geometry(d, prefix, actual_seq_qlen, actual_seq_kvlen, 0);
     std::vector<PagedGroup> groups;
     std::vector<PagedUnit> units;
@@ -604,6 +642,7 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
     const size_t seq_bytes = align_up(recs.size() * sizeof(SeqRec), 256);
     const size_t group_bytes = align_up(groups.size() * sizeof(PagedGroup), 256);
     const size_t payload = seq_bytes + group_bytes + units.size() * sizeof(PagedUnit);
+    retire_captured(h);
     st = ensure_workspace(h, align_up(kHeaderBytes + payload, 256) + units.size() * part_unit,
                           stream);
     if (st != FA_OK) return st;
@@ -611,10 +650,8 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
     if (st != FA_OK) return st;
     cudaError_t e = cudaEventSynchronize(h->stage_done);
     if (e != cudaSuccess) return cuda_fail(e, "cudaEventSynchronize");
-    if (h->any_call) {
-      e = cudaStreamWaitEvent(stream, h->last_call, 0);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
-    }
+    st = order_after_last(h, false, stream);
+    if (st != FA_OK) return st;
     uint8_t* hs = static_cast<uint8_t*>(h->h_stage);
     std::memcpy(hs, recs.data(), recs.size() * sizeof(SeqRec));
     if (!groups.empty()) std::memcpy(hs + seq_bytes, groups.data(), groups.size() * sizeof(PagedGroup));
@@ -634,10 +671,10 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
     h->n_items = 0;
     h->paged_rows = 0;
     for (const PagedGroup& g : groups) h->paged_rows = std::max(h->paged_rows, g.nrows);
-  } else if (h->any_call) {
-    // The partial buffer is rewritten: order after the handle's last call.
-    cudaError_t e = cudaStreamWaitEvent(stream, h->last_call, 0);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
+  } else {
+    // The partial buffer is rewritten.
+    st = order_after_last(h, capturing, stream);
+    if (st != FA_OK) return st;
   }
   if (h->n_groups == 0) return FA_OK;  // no query rows
   uint8_t* ws = static_cast<uint8_t*>(h->d_ws);
@@ -672,11 +709,8 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
   pp.scale_log2 = (float)(d->scale * 1.4426950408889634073599);
   cudaError_t e = launch_paged((int)D, h->paged_rows, pp, stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged kernel launch");
-  e = cudaEventRecord(h->last_call, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
-  h->any_call = true;
   failed.armed = false;
-  return FA_OK;
+  return record_call(h, capturing, stream);
 }
 
 fa_status_t fa_mask_occupancy(const fa_desc_t* desc, const uint8_t* atten_mask,
@@ -717,19 +751,26 @@ fa_status_t fa_mask_occupancy(const fa_desc_t* desc, const uint8_t* atten_mask,
 fa_status_t fa_sync_status(fa_handle_t h) {
   clear_error();
   if (!h) return fail(FA_ERR_NULLPTR, "handle is NULL");
-  if (!h->any_call) return FA_OK;
-  cudaError_t e = cudaEventSynchronize(h->last_call);
+  cudaError_t e = h->any_call ? cudaEventSynchronize(h->last_call) : cudaSuccess;
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventSynchronize");
-  if (h->d_ws == nullptr) return FA_OK;  // a call since then found no memory
   unsigned int word = 0;
-  e = cudaMemcpy(&word, h->d_ws, sizeof(word), cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(error word)");
+  // The workspace (none before the first call, or when one since then found
+  // no memory) and those that captured calls use.
+  std::vector<void*> all = h->retired;
+  if (h->d_ws != nullptr) all.push_back(h->d_ws);
+  for (void* ws : all) {
+    unsigned int w = 0;
+    e = cudaMemcpy(&w, ws, sizeof(w), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(error word)");
+    if (w == 0) continue;
+    word |= w;
+    // Clear the whole header: the error word and, should an aborted launch
+    // have left them set, the claim counters.
+    e = cudaMemset(ws, 0, kHeaderBytes);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // the next call may not wait for it
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(header)");
+  }
   if (word == 0) return FA_OK;
-  // Clear the whole header: the error word and, should an aborted launch
-  // have left them set, the claim counters.
-  e = cudaMemset(h->d_ws, 0, kHeaderBytes);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // the next call may not wait for it
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(header)");
   if (word & kErrTimeout)
     return fail(FA_ERR_TIMEOUT, "a device-side wait gave up (site %u); outputs are undefined",
                 (word >> kErrWhereShift) & 0xffu);
@@ -745,6 +786,7 @@ fa_status_t fa_destroy(fa_handle_t h) {
   if (h->any_call) cudaEventSynchronize(h->last_call);
   if (h->stage_done) cudaEventSynchronize(h->stage_done);
   if (h->d_ws) cudaFree(h->d_ws);
+  for (void* ws : h->retired) cudaFree(ws);
   if (h->h_stage) cudaFreeHost(h->h_stage);
   if (h->stage_done) cudaEventDestroy(h->stage_done);
   if (h->last_call) cudaEventDestroy(h->last_call);

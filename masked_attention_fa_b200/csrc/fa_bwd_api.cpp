@@ -39,12 +39,11 @@ fa_status_t ensure_buffer(fa_handle_t h, DeviceBuffer* buf, size_t bytes) {
 }
 
 fa_status_t refuse_capture(cudaStream_t stream) {
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  const cudaError_t e = cudaStreamIsCapturing(stream, &cap);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
-  if (cap != cudaStreamCaptureStatusNone)
+  bool capturing = false;
+  const fa_status_t st = stream_capturing(stream, &capturing);
+  if (st == FA_OK && capturing)
     return fail(FA_ERR_UNSUPPORTED, "this call cannot be captured into a graph");
-  return FA_OK;
+  return st;
 }
 
 void release_training(fa_handle_t h) {
@@ -78,12 +77,11 @@ fa_status_t validate_rel(const fa_desc_t* d, const fa_relbias_t* bias) {
 fa_status_t prepare_rel(fa_handle_t h, const fa_relbias_t* bias, cudaStream_t stream, RelBias* out,
                         RelTable* table) {
   const int32_t N = (int32_t)h->desc.N, R = bias->reach, row = rel_row(R);
-  if (h->any_call) {  // an earlier call on another stream may still read the tables
-    const cudaError_t e = cudaStreamWaitEvent(stream, h->last_call, 0);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
-  }
+  // An earlier call on another stream may still read the tables.
+  fa_status_t st = order_after_last(h, false, stream);
+  if (st != FA_OK) return st;
   const size_t entries = (size_t)(2 * R + 1);
-  fa_status_t st = ensure_buffer(h, &h->rel.ext, (size_t)N * 4 * row * sizeof(float));
+  st = ensure_buffer(h, &h->rel.ext, (size_t)N * 4 * row * sizeof(float));
   if (st != FA_OK) return st;
   std::vector<int32_t>& held = h->rel.bucket_of;
   if (held.size() != entries || !std::equal(held.begin(), held.end(), bias->bucket_of)) {
@@ -325,11 +323,8 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   if (st != FA_OK) return st;
   st = ensure_workspace(h, kHeaderBytes, stream);  // the error word
   if (st != FA_OK) return st;
-  cudaError_t e = cudaSuccess;
-  if (h->any_call) {  // lists and scratch are rewritten: order after the last call
-    e = cudaStreamWaitEvent(stream, h->last_call, 0);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
-  }
+  st = order_after_last(h, false, stream);  // lists and scratch are rewritten
+  if (st != FA_OK) return st;
   FailedCall failed{h, stream, true};
   st = refresh_lists(h, a.prefix, a.cu_q, a.cu_kv, has_mask, stream);
   if (st != FA_OK) return st;
@@ -459,7 +454,7 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   }
   p.claims = reinterpret_cast<unsigned int*>(scratch + stat_bytes + part_bytes + dist_bytes + done_bytes);
   p.n_claims = (int32_t)n_claims;
-  e = p.n_q > 0 ? launch_bwd_stats((int)d->D, p, m, stream)
+  cudaError_t e = p.n_q > 0 ? launch_bwd_stats((int)d->D, p, m, stream)
                 : cudaMemsetAsync(p.claims, 0, n_claims * sizeof(unsigned int), stream);
   if (e != cudaSuccess) return cuda_fail(e, "row statistics launch");
   const char* why = nullptr;
@@ -490,11 +485,8 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
       e = cudaMemsetAsync(a.dtable, 0, (size_t)a.bias->num_buckets * d->N * sizeof(float), stream);
     if (e != cudaSuccess) return cuda_fail(e, "bias gradient launch");
   }
-  e = cudaEventRecord(h->last_call, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
-  h->any_call = true;
   failed.armed = false;
-  return FA_OK;
+  return record_call(h, false, stream);
 }
 
 // No C++ exception leaves a C entry point.

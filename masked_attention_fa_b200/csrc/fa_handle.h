@@ -79,6 +79,10 @@ struct fa_handle_s {
   cudaEvent_t stage_done = nullptr;
   cudaEvent_t last_call = nullptr;
   bool any_call = false;
+  // A graph reads the workspace's list (see retire_captured); workspaces of
+  // earlier lists that graphs read.
+  bool captured = false;
+  std::vector<void*> retired;
   // tensor maps of the last call's operands
   const void* tm_key[3] = {nullptr, nullptr, nullptr};
   CUtensorMap tm[3];
@@ -113,6 +117,16 @@ fa_status_t ensure_workspace(fa_handle_t h, size_t bytes, cudaStream_t stream);
 // Grows a buffer to `bytes` (waiting for the handle's last call before the
 // old one is freed); its contents are lost.
 fa_status_t ensure_buffer(fa_handle_t h, DeviceBuffer* buf, size_t bytes);
+fa_status_t stream_capturing(cudaStream_t stream, bool* capturing);
+// Makes the stream wait for the handle's last call. Not in a capture: what
+// orders a replay is the stream it is launched on, and an event recorded
+// outside cannot be waited for inside.
+fa_status_t order_after_last(fa_handle_t h, bool capturing, cudaStream_t stream);
+// Notes the call that has just been enqueued as the handle's last. An event
+// recorded in a capture could not be waited for outside: a captured call is
+// none that later calls wait for.
+fa_status_t record_call(fa_handle_t h, bool capturing, cudaStream_t stream);
+void retire_captured(fa_handle_t h);
 // Calls whose tables are uploaded or rebuilt per call are not captured into
 // graphs: a replay would read another call's.
 fa_status_t refuse_capture(cudaStream_t stream);
