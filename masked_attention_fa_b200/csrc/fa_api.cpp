@@ -37,6 +37,7 @@ bool env_flag(const char* name) {
 }
 
 fa_status_t cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();  // reported here: the next call's launches do not find it
   return fail(FA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
@@ -156,11 +157,12 @@ fa_status_t ensure_workspace(fa_handle_t h, size_t bytes, cudaStream_t stream) {
     h->ws_bytes = 0;
   }
   h->plan_valid = false;
-  if (env_flag("FA_TEST_FAIL_ALLOC")) return fail(FA_ERR_ALLOC, "device workspace (test hook)");
   size_t want = align_up(bytes < 4096 ? 4096 : bytes, 4096);
+  if (env_flag("FA_TEST_FAIL_ALLOC")) want = (size_t)1 << 60;  // more than there is
   cudaError_t e = cudaMalloc(&h->d_ws, want);
   if (e != cudaSuccess) {
     h->d_ws = nullptr;
+    cudaGetLastError();
     return fail(FA_ERR_ALLOC, "cudaMalloc(%zu): %s", want, cudaGetErrorString(e));
   }
   e = cudaMemsetAsync(h->d_ws, 0, kHeaderBytes, stream);
@@ -185,6 +187,7 @@ fa_status_t ensure_stage(fa_handle_t h, size_t bytes) {
   cudaError_t e = cudaMallocHost(&h->h_stage, want);
   if (e != cudaSuccess) {
     h->h_stage = nullptr;
+    cudaGetLastError();
     return fail(FA_ERR_ALLOC, "cudaMallocHost(%zu): %s", want, cudaGetErrorString(e));
   }
   h->stage_bytes = want;

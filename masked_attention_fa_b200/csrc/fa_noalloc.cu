@@ -99,6 +99,7 @@ uint64_t wait_limit_ns() {
 }
 
 fa_status_t cuda_err(cudaError_t e, const char* what) {
+  cudaGetLastError();  // reported here: the next call's launches do not find it
   return fail(FA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
