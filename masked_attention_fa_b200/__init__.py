@@ -511,6 +511,7 @@ class MaskedAttention:
             return self._relbias_forward(q, k, v, rel_bias, rel_buckets, atten_mask, ranges,
                                          slopes, prefix, actual_seq_qlen, actual_seq_kvlen, out,
                                          lse, stream)
+        self._no_mask_beside(slopes, atten_mask, ranges)
         oshape, lshape = self.out_shapes()
         if out is None:
             out = torch.empty(oshape, dtype=torch.bfloat16, device=q.device)
@@ -560,6 +561,14 @@ class MaskedAttention:
             pass
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape "
                          f"{tuple(shape)} on {device}")
+
+    def _no_mask_beside(self, slopes, atten_mask, ranges=None):
+        """An ALiBi call reads no attenMask: one that sparse mode 0 would read is
+        refused (the other modes a handle with slopes can have ignore it)."""
+        if slopes is None:
+            return
+        if ranges is not None or (atten_mask is not None and self.desc.sparse_mode <= 1):
+            raise ValueError("slopes go with neither ranges nor, in sparse mode 0, an atten_mask")
 
     def _need_bias(self, device, rel_bias, rel_buckets):
         import torch
@@ -628,6 +637,7 @@ class MaskedAttention:
         fa_bwd in include/fa.h). d_o, d_lse: the gradients of o and lse (d_lse
         None: 0)."""
         import torch
+        self._no_mask_beside(slopes, atten_mask)
         bf16, f32, dev, need = torch.bfloat16, torch.float32, q.device, self._need
         oshape, kshape, lshape = self._oshape, self._kshape, self._lshape
         need("q", q, oshape, bf16, dev)
