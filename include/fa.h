@@ -269,14 +269,19 @@ fa_status_t fa_fwd_relbias(fa_handle_t h, const void* q, const void* k, const vo
  * forward rounds P; all sums are fp32. Results are bitwise deterministic: every
  * sum has one fixed order, at the price of computing the scores twice, or of
  * writing dS (bf16) to memory once: with D = 128 and more than 4 work items (128
- * query rows or keys of a head) per SM.
+ * query rows or keys of a head) per SM. Which of the two is decided when the
+ * handle meets new lengths, prefixes or the first mask, and kept for calls that
+ * repeat them; it changes the order of dq's sums, and so its bits, but not dk's,
+ * dv's or dtable's.
  * The handle's work lists for the backward are kept beside the forward's, so
  * alternating the two rebuilds neither. Device workspace, grown on the first
- * calls: 1 KiB per 128 query rows and head, about 130 bytes per 128 rows or
- * keys and head, for a dense mask 2 bits per pair, and where dS is written 32
- * KiB per pair of 128 rows and 128 keys that see each other, of the heads held
- * at once: at most 4 GiB (a call whose single head needs more, or that cannot
- * have the memory, computes the scores twice).
+ * calls, outside any allocator of the caller's and kept until fa_destroy: 1 KiB
+ * per 128 query rows and head, about 130 bytes per 128 rows or keys and head,
+ * for a dense mask 2 bits per pair, and where dS is written 32 KiB per pair of
+ * 128 rows and 128 keys that see each other, of the heads held at once: at most
+ * 4 GiB a handle, less where there is no more memory (fewer heads at once, with
+ * the same results). A call whose single head needs more, or does not get its
+ * room, computes the scores twice.
  * Errors: fa_fwd's, and FA_ERR_PARAM_INVALID for a handle that names an ALiBi
  * variant (fa_bwd_alibi), FA_ERR_UNSUPPORTED on a stream that is being
  * captured into a graph (the work lists would be another call's at replay).

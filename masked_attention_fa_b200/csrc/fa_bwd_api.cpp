@@ -135,13 +135,36 @@ void order_items(std::vector<BwdItem>::iterator first, std::vector<BwdItem>::ite
   });
 }
 
+// Room for `tiles` tiles of dS.
+bool room_for_ds(fa_handle_t h, int64_t tiles) {
+  if (const char* t = std::getenv("FA_TEST_SPILL_ROOM"))
+    if (tiles > std::atoll(t)) return false;
+  if (ensure_buffer(h, &h->bwd.spill, (size_t)tiles * 128 * 128 * 2) == FA_OK) return true;
+  clear_error();
+  return false;
+}
+
+// The most tiles of dS held at once when heads are taken in order into shares
+// of at most `cap` tiles; need[b] is a head's of sequence b.
+int64_t largest_share(const std::vector<int64_t>& need, int64_t N, int64_t cap) {
+  int64_t most = 0, used = 0;
+  for (int64_t n : need) {
+    for (int64_t hd = 0; hd < N; ++hd) {
+      if (used + n > cap) used = 0;
+      used += n;
+      most = std::max(most, used);
+    }
+  }
+  return most;
+}
+
 // Builds and uploads the lists of this call's lengths unless the handle
-// holds them already.
+// holds them already. Where dS is written, its room is found here, so that a
+// call keeps its way of working, and its bits, until the lengths change.
 fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* cu_q,
                           const int64_t* cu_kv, int has_mask, cudaStream_t stream) {
   BwdState& bw = h->bwd;
   std::vector<int64_t> key = make_key(&h->desc, prefix, cu_q, cu_kv, has_mask);
-  key.push_back(bw.no_spill);
   if (bw.valid && key == bw.key) return FA_OK;
   const std::vector<SeqRec> recs = decode_geometry(&h->desc, prefix, cu_q, cu_kv, has_mask);
   const int32_t N = (int32_t)h->desc.N;
@@ -152,14 +175,38 @@ fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* c
   }
   if (std::max(tiles, k_tiles) * N > 0x3fffffff)
     return fail(FA_ERR_UNSUPPORTED, "too many work items");
+  std::vector<TileRange> kr;       // of every key tile, sequence by sequence
+  std::vector<int64_t> need;       // tiles of dS of one head; a mask's are not known here
+  kr.reserve((size_t)k_tiles);
+  need.reserve(recs.size());
+  for (const SeqRec& s : recs) {
+    const int32_t nq = (s.sq + kTileM - 1) / kTileM, nk = (s.skv + kTileN - 1) / kTileN;
+    int64_t n = 0;
+    for (int32_t t = 0; t < nk; ++t) {
+      kr.push_back(key_tile_rows(s, (int64_t)t * kTileN));
+      n += has_mask ? nq : kr.back().hi - kr.back().lo;
+    }
+    need.push_back(n);
+  }
   // Two products less against 32 KB written and read a pair of tiles, and one
   // after the other instead of side by side. Causal, D = 128: 16 heads x 2048
   // (512 items) 71 us with dS written, 68 by two walks, 8 heads x 2048 60 and
   // 45, but 32 heads x 2048 (1,024 items) 136 and 149, 32 x 4096 430 and 459.
   // At D = 64 the products weigh half: 651 and 610 us on the bias backward of
   // 32 heads x 4096.
-  bool spill = !bw.no_spill && h->desc.D == 128 && (tiles + k_tiles) * N > 4 * h->num_sms;
-  const int64_t cap = spill_tiles();
+  bool spill = h->desc.D == 128 && (tiles + k_tiles) * N > 4 * h->num_sms;
+  bw.valid = false;
+  // Shares as large as there is memory for: their size changes no bit. When
+  // there is none for one head's, two walks.
+  int64_t cap = spill_tiles();
+  const int64_t head = need.empty() ? 0 : *std::max_element(need.begin(), need.end());
+  if (head > cap) spill = false;
+  while (spill && head > 0) {
+    const int64_t most = largest_share(need, N, cap);
+    if (room_for_ds(h, most)) break;
+    if (most <= head) spill = false;
+    else cap = std::max(head, most / 2);
+  }
   std::vector<BwdItem> qi, ki, gi;
   std::vector<KeySpan> spans((size_t)(k_tiles * N));
   qi.reserve((size_t)(tiles * N));
@@ -169,29 +216,24 @@ fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* c
   for (size_t b = 0; b < recs.size(); ++b) {
     const SeqRec& s = recs[b];
     const int32_t nq = (s.sq + kTileM - 1) / kTileM, nk = (s.skv + kTileN - 1) / kTileN;
-    std::vector<TileRange> qr((size_t)nq), kr((size_t)nk);
+    std::vector<TileRange> qr((size_t)nq);
     for (int32_t t = 0; t < nq; ++t) qr[t] = tile_range(s, (int64_t)t * kTileM);
-    int64_t need = 0;  // tiles of dS of one head; a mask's are not known here
-    for (int32_t t = 0; t < nk; ++t) {
-      kr[t] = key_tile_rows(s, (int64_t)t * kTileN);
-      need += has_mask ? nq : kr[t].hi - kr[t].lo;
-    }
-    if (need > cap) spill = false;
+    const TileRange* kt = kr.data() + k_base;
     for (int32_t hd = 0; hd < N; ++hd) {
       for (int32_t t = 0; t < nq; ++t)
         qi.push_back(BwdItem{(int32_t)b, hd, t, (int32_t)(hd * tiles + q_base + t), qr[t].lo,
                              qr[t].hi, qr[t].full_lo, qr[t].full_hi, 0, {0, 0, 0}});
-      if (spill && (chunks.empty() || used + need > cap)) {
+      if (spill && (chunks.empty() || used + need[b] > cap)) {
         chunks.push_back(
             {(int32_t)ki.size(), (int32_t)ki.size(), (int32_t)gi.size(), (int32_t)gi.size(), 0});
         used = 0;
       }
       const int32_t span = (int32_t)(hd * k_tiles + k_base);
       for (int32_t t = 0; t < nk; ++t) {
-        ki.push_back(BwdItem{(int32_t)b, hd, t, (int32_t)(hd * tiles + q_base), kr[t].lo, kr[t].hi,
-                             kr[t].full_lo, kr[t].full_hi, span + t, {0, 0, 0}});
-        spans[span + t] = KeySpan{(int32_t)(has_mask ? used : used - kr[t].lo), kr[t].lo, kr[t].hi, 0};
-        used += has_mask ? nq : kr[t].hi - kr[t].lo;
+        ki.push_back(BwdItem{(int32_t)b, hd, t, (int32_t)(hd * tiles + q_base), kt[t].lo, kt[t].hi,
+                             kt[t].full_lo, kt[t].full_hi, span + t, {0, 0, 0}});
+        spans[span + t] = KeySpan{(int32_t)(has_mask ? used : used - kt[t].lo), kt[t].lo, kt[t].hi, 0};
+        if (spill) used += has_mask ? nq : kt[t].hi - kt[t].lo;
       }
       for (int32_t t = 0; spill && t < nq; t += 2) {
         TileRange r = qr[t];
@@ -210,10 +252,6 @@ fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* c
     q_base += nq;
     k_base += nk;
   }
-  if (!spill) {
-    chunks.clear();
-    gi.clear();
-  }
   order_items(qi.begin(), qi.end(), h->num_sms);
   if (!spill) order_items(ki.begin(), ki.end(), h->num_sms);
   for (const BwdState::Chunk& c : chunks) {
@@ -225,7 +263,6 @@ fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* c
   const size_t k_bytes = align_up(ki.size() * sizeof(BwdItem), 256);
   const size_t g_bytes = align_up(gi.size() * sizeof(BwdItem), 256);
   const size_t total = seq_bytes + q_bytes + k_bytes + g_bytes + spans.size() * sizeof(KeySpan);
-  bw.valid = false;
   fa_status_t st = ensure_buffer(h, &bw.lists, total);
   if (st != FA_OK) return st;
   bw.host.assign(total, 0);
@@ -330,13 +367,6 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   if (st != FA_OK) return st;
   int64_t ds_tiles = 0;
   for (const BwdState::Chunk& c : h->bwd.chunks) ds_tiles = std::max(ds_tiles, c.tiles);
-  if (ds_tiles > 0 && ensure_buffer(h, &h->bwd.spill, (size_t)ds_tiles * 128 * 128 * 2) != FA_OK) {
-    clear_error();  // no room for dS: the walks that need none
-    h->bwd.no_spill = true;
-    st = refresh_lists(h, a.prefix, a.cu_q, a.cu_kv, has_mask, stream);
-    if (st != FA_OK) return st;
-    ds_tiles = 0;
-  }
   const BwdState& bw = h->bwd;
 
   // Scratch: row statistics | bias sums by tile and by distance, counters |

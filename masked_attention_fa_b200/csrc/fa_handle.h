@@ -33,7 +33,6 @@ struct BwdState {
     int64_t tiles;
   };
   std::vector<Chunk> chunks;
-  bool no_spill = false;     // there was no room for dS
   SeqRec geo0{};             // geometry of sequence 0
   std::vector<uint8_t> host; // the uploaded lists
   DeviceBuffer lists;        // [SeqRec x B][BwdItem x n_q][x n_k][x n_g][KeySpan x k_tiles N]
