@@ -98,6 +98,8 @@ fa_status_t bind_device(fa_handle_t h) {
                 major, minor);
   e = cudaEventCreateWithFlags(&h->stage_done, cudaEventDisableTiming);
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventCreate");
+  e = cudaEventCreateWithFlags(&h->bwd.stage_done, cudaEventDisableTiming);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaEventCreate");
   e = cudaEventCreateWithFlags(&h->last_call, cudaEventDisableTiming);
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventCreate");
   h->device = dev;
@@ -173,28 +175,27 @@ fa_status_t ensure_workspace(fa_handle_t h, size_t bytes, cudaStream_t stream) {
 
 }  // namespace fa
 
-namespace {
+namespace fa {
 
-fa_status_t ensure_stage(fa_handle_t h, size_t bytes) {
-  if (h->h_stage != nullptr && h->stage_bytes >= bytes) return FA_OK;
-  if (h->h_stage != nullptr) {
-    cudaEventSynchronize(h->stage_done);
-    cudaFreeHost(h->h_stage);
-    h->h_stage = nullptr;
-    h->stage_bytes = 0;
-  }
-  size_t want = align_up(bytes < 4096 ? 4096 : bytes, 4096);
-  cudaError_t e = cudaMallocHost(&h->h_stage, want);
+fa_status_t ensure_pinned(void** stage, size_t* have, cudaEvent_t done, size_t bytes) {
+  const cudaError_t s = cudaEventSynchronize(done);
+  if (s != cudaSuccess) return cuda_fail(s, "cudaEventSynchronize");
+  if (*stage != nullptr && *have >= bytes) return FA_OK;
+  if (*stage != nullptr) cudaFreeHost(*stage);
+  *stage = nullptr;
+  *have = 0;
+  const size_t want = align_up(bytes < 4096 ? 4096 : bytes, 4096);
+  const cudaError_t e = cudaMallocHost(stage, want);
   if (e != cudaSuccess) {
-    h->h_stage = nullptr;
+    *stage = nullptr;
     cudaGetLastError();
     return fail(FA_ERR_ALLOC, "cudaMallocHost(%zu): %s", want, cudaGetErrorString(e));
   }
-  h->stage_bytes = want;
+  *have = want;
   return FA_OK;
 }
 
-}  // namespace
+}  // namespace fa
 
 namespace fa {
 
@@ -251,10 +252,8 @@ fa_status_t refresh_plan(fa_handle_t h, const int64_t* prefix, const int64_t* cu
                 : kHeaderBytes + payload,
       stream);
   if (st != FA_OK) return st;
-  st = ensure_stage(h, payload);
+  st = ensure_pinned(&h->h_stage, &h->stage_bytes, h->stage_done, payload);
   if (st != FA_OK) return st;
-  cudaError_t e = cudaEventSynchronize(h->stage_done);  // previous upload has left staging
-  if (e != cudaSuccess) return cuda_fail(e, "cudaEventSynchronize");
   // A kernel of this handle on another stream may still read the old list.
   st = order_after_last(h, false, stream);
   if (st != FA_OK) return st;
@@ -272,7 +271,7 @@ fa_status_t refresh_plan(fa_handle_t h, const int64_t* prefix, const int64_t* cu
     }
   }
   h->plan_valid = false;  // until the new one is whole
-  e = cudaMemcpyAsync(static_cast<uint8_t*>(h->d_ws) + kHeaderBytes, hs, payload,
+  cudaError_t e = cudaMemcpyAsync(static_cast<uint8_t*>(h->d_ws) + kHeaderBytes, hs, payload,
                       cudaMemcpyHostToDevice, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyAsync(work list)");
   e = cudaEventRecord(h->stage_done, stream);
@@ -649,10 +648,8 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
     st = ensure_workspace(h, align_up(kHeaderBytes + payload, 256) + units.size() * part_unit,
                           stream);
     if (st != FA_OK) return st;
-    st = ensure_stage(h, payload);
+    st = ensure_pinned(&h->h_stage, &h->stage_bytes, h->stage_done, payload);
     if (st != FA_OK) return st;
-    cudaError_t e = cudaEventSynchronize(h->stage_done);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaEventSynchronize");
     st = order_after_last(h, false, stream);
     if (st != FA_OK) return st;
     uint8_t* hs = static_cast<uint8_t*>(h->h_stage);
@@ -661,7 +658,7 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
     if (!units.empty())
       std::memcpy(hs + seq_bytes + group_bytes, units.data(), units.size() * sizeof(PagedUnit));
     h->plan_valid = false;
-    e = cudaMemcpyAsync(static_cast<uint8_t*>(h->d_ws) + kHeaderBytes, hs, payload,
+    cudaError_t e = cudaMemcpyAsync(static_cast<uint8_t*>(h->d_ws) + kHeaderBytes, hs, payload,
                         cudaMemcpyHostToDevice, stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyAsync(paged work list)");
     e = cudaEventRecord(h->stage_done, stream);

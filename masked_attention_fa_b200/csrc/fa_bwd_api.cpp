@@ -50,6 +50,11 @@ void release_training(fa_handle_t h) {
   for (DeviceBuffer* b : {&h->bwd.lists, &h->bwd.scratch, &h->bwd.spill, &h->rel.map, &h->rel.ext,
                           &h->rel.rows})
     if (b->ptr) cudaFree(b->ptr);
+  if (h->bwd.stage_done) {
+    cudaEventSynchronize(h->bwd.stage_done);
+    cudaEventDestroy(h->bwd.stage_done);
+  }
+  if (h->bwd.stage) cudaFreeHost(h->bwd.stage);
 }
 
 fa_status_t validate_rel(const fa_desc_t* d, const fa_relbias_t* bias) {
@@ -265,8 +270,9 @@ fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* c
   const size_t total = seq_bytes + q_bytes + k_bytes + g_bytes + spans.size() * sizeof(KeySpan);
   fa_status_t st = ensure_buffer(h, &bw.lists, total);
   if (st != FA_OK) return st;
-  bw.host.assign(total, 0);
-  uint8_t* at = bw.host.data();
+  st = ensure_pinned(&bw.stage, &bw.stage_bytes, bw.stage_done, total);
+  if (st != FA_OK) return st;
+  uint8_t* at = static_cast<uint8_t*>(bw.stage);
   auto put = [&](const void* src, size_t bytes, size_t room) {
     if (bytes) std::memcpy(at, src, bytes);
     at += room;
@@ -276,10 +282,10 @@ fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* c
   put(ki.data(), ki.size() * sizeof(BwdItem), k_bytes);
   put(gi.data(), gi.size() * sizeof(BwdItem), g_bytes);
   put(spans.data(), spans.size() * sizeof(KeySpan), 0);
-  // Pageable memory: the call returns once the source has been read.
-  const cudaError_t e =
-      cudaMemcpyAsync(bw.lists.ptr, bw.host.data(), total, cudaMemcpyHostToDevice, stream);
+  cudaError_t e = cudaMemcpyAsync(bw.lists.ptr, bw.stage, total, cudaMemcpyHostToDevice, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyAsync(backward lists)");
+  e = cudaEventRecord(bw.stage_done, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
   bw.key.swap(key);
   bw.valid = true;
   bw.n_q = (int32_t)qi.size();

@@ -34,7 +34,11 @@ struct BwdState {
   };
   std::vector<Chunk> chunks;
   SeqRec geo0{};             // geometry of sequence 0
-  std::vector<uint8_t> host; // the uploaded lists
+  // Pinned staging of the lists (beside the forward's, so that neither waits
+  // for the other's upload) and the event of their last upload.
+  void* stage = nullptr;
+  size_t stage_bytes = 0;
+  cudaEvent_t stage_done = nullptr;
   DeviceBuffer lists;        // [SeqRec x B][BwdItem x n_q][x n_k][x n_g][KeySpan x k_tiles N]
   DeviceBuffer scratch;      // row statistics, dense-mask ranges, bias sums
   DeviceBuffer spill;        // dS
@@ -129,6 +133,8 @@ void retire_captured(fa_handle_t h);
 // Calls whose tables are uploaded or rebuilt per call are not captured into
 // graphs: a replay would read another call's.
 fa_status_t refuse_capture(cudaStream_t stream);
+// Waits for the last upload from a pinned buffer and gives it at least `bytes`.
+fa_status_t ensure_pinned(void** stage, size_t* have, cudaEvent_t done, size_t bytes);
 // Frees what the backward and the relative position bias hold.
 void release_training(fa_handle_t h);
 // The handle's copy of the bias by distance (see RelBias) and what lays it out
