@@ -133,6 +133,10 @@ struct __align__(64) BwdParams {
   uint64_t timeout_ns;
 };
 
+// Head dims at which dS may be written out (the host's rule and what it
+// measured: refresh_lists); the kernels of the others have no code for it.
+constexpr bool bwd_may_write_ds(int64_t D) { return D == 128; }
+
 // dQ, dK, dV and rel_part.
 //
 // Without p.ds by two walks that need nothing of each other: dQ by query tiles

@@ -199,7 +199,7 @@ fa_status_t refresh_lists(fa_handle_t h, const int64_t* prefix, const int64_t* c
   // 45, but 32 heads x 2048 (1,024 items) 136 and 149, 32 x 4096 430 and 459.
   // At D = 64 the products weigh half: 651 and 610 us on the bias backward of
   // 32 heads x 4096.
-  bool spill = h->desc.D == 128 && (tiles + k_tiles) * N > 4 * h->num_sms;
+  bool spill = bwd_may_write_ds(h->desc.D) && (tiles + k_tiles) * N > 4 * h->num_sms;
   bw.valid = false;
   // Shares as large as there is memory for: their size changes no bit. When
   // there is none for one head's, two walks.

@@ -89,6 +89,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // needs less (0: 457, 3: 463 us on a causal 2 x 16 x 4096 x 128).
 template <int D>
 constexpr int kPolyOf8 = D == 64 ? 2 : 0;
+template <int D>
+constexpr bool kWritesDs = bwd_may_write_ds(D);
 
 // Where a wait gave up (error word bits 8..15), after the forward's sites.
 enum BwdSite : uint32_t {
@@ -655,7 +657,7 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
     // Spilled dS: this thread's first 8 columns in the item's tile t = 0.
     __nv_bfloat16* ds_out = nullptr;
     bool ragged = false;
-    if (kKeys && p.ds) {
+    if (kKeys && kWritesDs<D> && p.ds) {
       ds_out = p.ds + (int64_t)p.spans[it.span].first * (128 * 128) + g * (kCols * 128) + row * 8;
       ragged = (it.tile + 1) * 128 > sr.skv;
     }
@@ -833,7 +835,7 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
           mbar_arrive(&ctl->ds_full);
           if (kKeys) mbar_arrive(&ctl->stat_empty[n & 1u]);
         }
-        if (kKeys && ds_out) {
+        if (kKeys && kWritesDs<D> && ds_out) {
           // Rows past the sequence's end go out as zeros, dQ sums over them.
           if (ragged && !stored) {
 #pragma unroll
@@ -1171,7 +1173,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
   // What is above ran beside the launch ahead of this one; what is below reads
   // its results, but for the key walk behind a query walk: the two need nothing
   // of each other, and each SM that is free may start on it.
-  if (!kKeys || p.ds) asm volatile("griddepcontrol.wait;" ::: "memory");
+  const bool writes_ds = kWritesDs<D> && p.ds != nullptr;
+  if (!kKeys || writes_ds) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const WaitCtx w{&ctl->abort_flag, p.err_word, p.timeout_ns};
   if (warp < kMathWarps) {
@@ -1198,7 +1201,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_sm100(const __grid_cons
   }
   // The key walk may have started beside the query walk: it ends after it,
   // so that what follows in the stream follows both.
-  if (kKeys && !p.ds) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (kKeys && !writes_ds) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------- dQ from dS
@@ -1554,10 +1557,14 @@ static cudaError_t launch_dq(const BwdParams& p, int num_sms, cudaStream_t strea
 template <int D, int kBias>
 static cudaError_t launch_walks(const BwdParams& p, int num_sms, cudaStream_t stream,
                                 const char** why) {
-  cudaError_t e = p.ds ? cudaSuccess : launch_walk<D, false, kBias>(p, num_sms, stream, why);
-  if (e == cudaSuccess) e = launch_walk<D, true, kBias>(p, num_sms, stream, why);
-  if (e == cudaSuccess && p.ds) e = launch_dq<D>(p, num_sms, stream, why);
-  return e;
+  if constexpr (dev::kWritesDs<D>) {
+    if (p.ds) {
+      const cudaError_t e = launch_walk<D, true, kBias>(p, num_sms, stream, why);
+      return e == cudaSuccess ? launch_dq<D>(p, num_sms, stream, why) : e;
+    }
+  }
+  const cudaError_t e = launch_walk<D, false, kBias>(p, num_sms, stream, why);
+  return e == cudaSuccess ? launch_walk<D, true, kBias>(p, num_sms, stream, why) : e;
 }
 
 cudaError_t launch_bwd(int D, const BwdParams& p, int num_sms, cudaStream_t stream,
