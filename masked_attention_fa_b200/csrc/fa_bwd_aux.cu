@@ -239,8 +239,8 @@ __global__ void __launch_bounds__(256) bwd_ranges(BwdMaskParams a) {
 // dist[h][e] = sum over head h's key tiles, in 64 bits: one CTA per head and
 // 32 distances, warp w adds tiles w, w + 8, ... and the eight sums are added
 // in warp order. The last CTA of a head to finish then sums the distances of
-// each bucket, those past the reach with the end they clip to: one warp per
-// bucket. Every order is fixed.
+// each bucket, those past the reach with the end they clip to, in 64 bits too:
+// one warp per bucket. Every order is fixed.
 __global__ void __launch_bounds__(256) rel_reduce(const float* __restrict__ part, double* dist,
                                                   unsigned int* done,
                                                   const int32_t* __restrict__ bucket_of,
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) rel_reduce(const float* __restrict__ part
                                                   int reach, int num_buckets) {
   __shared__ double sm[8][32];
   constexpr int kRoom = (2 * kRelMaxReach + 1 + 2 * kRelPad + 127) / 128 * 128;
-  __shared__ float by_dist[kRoom];
+  __shared__ double by_dist[kRoom];  // 64 bits: distances of a bucket may cancel
   __shared__ int32_t bucket[kRoom];
   __shared__ bool last;
   const int W = rel_width(reach);
@@ -274,19 +274,19 @@ __global__ void __launch_bounds__(256) rel_reduce(const float* __restrict__ part
   __threadfence();
   const int padded = (W + 127) / 128 * 128;
   for (int e = threadIdx.x; e < padded; e += 256) {
-    by_dist[e] = e < W ? (float)__ldcg(dist + (int64_t)h * W + e) : 0.f;
+    by_dist[e] = e < W ? __ldcg(dist + (int64_t)h * W + e) : 0.0;
     bucket[e] = e < W ? bucket_of[min(max(e - kRelPad, 0), 2 * reach)] : -1;
   }
   __syncthreads();
   for (int c = w; c < num_buckets; c += 8) {
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    double a[4] = {0.0, 0.0, 0.0, 0.0};
     for (int e = lane; e < padded; e += 128)
 #pragma unroll
-      for (int y = 0; y < 4; ++y) a[y] += bucket[e + 32 * y] == c ? by_dist[e + 32 * y] : 0.f;
-    float sum = (a[0] + a[1]) + (a[2] + a[3]);
+      for (int y = 0; y < 4; ++y) a[y] += bucket[e + 32 * y] == c ? by_dist[e + 32 * y] : 0.0;
+    double sum = (a[0] + a[1]) + (a[2] + a[3]);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    if (lane == 0) dtable[(int64_t)c * N + h] = sum;
+    if (lane == 0) dtable[(int64_t)c * N + h] = (float)sum;
   }
 }
 
