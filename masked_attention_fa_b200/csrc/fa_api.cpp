@@ -407,7 +407,7 @@ namespace {
 fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
                     const uint8_t* atten_mask, const int32_t* ranges, const float* slopes,
                     const fa_relbias_t* bias, const int64_t* prefix, const int64_t* actual_seq_qlen,
-                    const int64_t* actual_seq_kvlen, void* o, float* lse, void* cuda_stream) {
+                    const int64_t* actual_seq_kvlen, void* o, float* lse, void* cuda_stream) try {
   if (!h) return fail(FA_ERR_NULLPTR, "handle is NULL");
   if (!q || !k || !v || !o || !lse) return fail(FA_ERR_NULLPTR, "q, k, v, o and lse are required");
   const fa_desc_t* d = &h->desc;
@@ -541,6 +541,8 @@ fa_status_t forward(fa_handle_t h, const void* q, const void* k, const void* v,
   }
   failed.armed = false;
   return record_call(h, capturing, stream);
+} catch (const std::exception& e) {
+  return host_exception(e);
 }
 
 }  // namespace
@@ -577,12 +579,8 @@ fa_status_t fa_fwd_relbias(fa_handle_t h, const void* q, const void* k, const vo
   if (!h) return fail(FA_ERR_NULLPTR, "handle is NULL");
   fa_status_t st = validate_rel(&h->desc, bias);
   if (st != FA_OK) return st;
-  try {
-    return forward(h, q, k, v, nullptr, nullptr, nullptr, bias, prefix, actual_seq_qlen,
-                   actual_seq_kvlen, o, lse, cuda_stream);
-  } catch (const std::exception& e) {
-    return fail(FA_ERR_ALLOC, "host allocation: %s", e.what());
-  }
+  return forward(h, q, k, v, nullptr, nullptr, nullptr, bias, prefix, actual_seq_qlen,
+                 actual_seq_kvlen, o, lse, cuda_stream);
 }
 
 fa_status_t fa_fwd_with_ranges(fa_handle_t h, const void* q, const void* k, const void* v,
@@ -603,7 +601,7 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
                          const int32_t* block_table, int64_t num_blocks, int32_t block_size,
                          int32_t max_blocks, const int64_t* prefix, const int64_t* actual_seq_qlen,
                          const int64_t* actual_seq_kvlen, void* o, float* lse,
-                         void* cuda_stream) {
+                         void* cuda_stream) try {
   clear_error();
   if (!h) return fail(FA_ERR_NULLPTR, "handle is NULL");
   if (!q || !k_cache || !v_cache || !block_table || !o || !lse)
@@ -711,10 +709,12 @@ fa_status_t fa_fwd_paged(fa_handle_t h, const void* q, const void* k_cache, cons
   if (e != cudaSuccess) return cuda_fail(e, "paged kernel launch");
   failed.armed = false;
   return record_call(h, capturing, stream);
+} catch (const std::exception& e) {
+  return host_exception(e);
 }
 
 fa_status_t fa_mask_occupancy(const fa_desc_t* desc, const uint8_t* atten_mask,
-                              uint8_t* tile_class, int32_t* ranges, void* cuda_stream) {
+                              uint8_t* tile_class, int32_t* ranges, void* cuda_stream) try {
   clear_error();
   if (!desc) return fail(FA_ERR_NULLPTR, "desc is NULL");
   if (!atten_mask || !tile_class || !ranges)
@@ -746,9 +746,11 @@ fa_status_t fa_mask_occupancy(const fa_desc_t* desc, const uint8_t* atten_mask,
   e = launch_occupancy(a, sms, static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return cuda_fail(e, "occupancy pre-pass launch");
   return FA_OK;
+} catch (const std::exception& e) {
+  return host_exception(e);
 }
 
-fa_status_t fa_sync_status(fa_handle_t h) {
+fa_status_t fa_sync_status(fa_handle_t h) try {
   clear_error();
   if (!h) return fail(FA_ERR_NULLPTR, "handle is NULL");
   cudaError_t e = h->any_call ? cudaEventSynchronize(h->last_call) : cudaSuccess;
@@ -778,6 +780,8 @@ fa_status_t fa_sync_status(fa_handle_t h) {
     return fail(FA_ERR_DEVICE,
                 "a block_table entry was outside [0, num_blocks); its keys were left out");
   return fail(FA_ERR_DEVICE, "device error word 0x%08x", word);
+} catch (const std::exception& e) {
+  return host_exception(e);
 }
 
 fa_status_t fa_destroy(fa_handle_t h) {

@@ -525,13 +525,10 @@ fa_status_t enqueue_backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream)
   return record_call(h, false, stream);
 }
 
-// No C++ exception leaves a C entry point.
-fa_status_t backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream) {
-  try {
-    return enqueue_backward(h, a, cuda_stream);
-  } catch (const std::exception& e) {
-    return fail(FA_ERR_ALLOC, "host allocation: %s", e.what());
-  }
+fa_status_t backward(fa_handle_t h, const BwdArgs& a, void* cuda_stream) try {
+  return enqueue_backward(h, a, cuda_stream);
+} catch (const std::exception& e) {
+  return host_exception(e);
 }
 
 }  // namespace

@@ -26,8 +26,16 @@ fa_status_t fail(fa_status_t st, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
-  g_last_error = buf;
+  try {
+    g_last_error = buf;
+  } catch (const std::exception&) {  // no room for the message: the status alone
+    g_last_error.clear();
+  }
   return st;
+}
+
+fa_status_t host_exception(const std::exception& e) {
+  return fail(FA_ERR_ALLOC, "host allocation: %s", e.what());
 }
 
 void clear_error() { g_last_error.clear(); }
@@ -566,14 +574,16 @@ int32_t fa_version(void) { return FA_VERSION; }
 
 fa_status_t fa_validate(const fa_desc_t* desc, const int64_t* prefix,
                         const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
-                        int32_t has_mask) {
+                        int32_t has_mask) try {
   clear_error();
   return validate_call(desc, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask);
+} catch (const std::exception& e) {
+  return host_exception(e);
 }
 
 fa_status_t fa_visible_pairs(const fa_desc_t* desc, const int64_t* prefix,
                              const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
-                             int32_t has_mask, int64_t* pairs_out) {
+                             int32_t has_mask, int64_t* pairs_out) try {
   clear_error();
   if (!pairs_out) return fail(FA_ERR_NULLPTR, "pairs_out is NULL");
   fa_status_t st = validate_call(desc, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask);
@@ -583,11 +593,13 @@ fa_status_t fa_visible_pairs(const fa_desc_t* desc, const int64_t* prefix,
   auto recs = decode_geometry(desc, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask);
   *pairs_out = visible_pairs(desc, recs);
   return FA_OK;
+} catch (const std::exception& e) {
+  return host_exception(e);
 }
 
 int32_t fa_tile_class(const fa_desc_t* desc, const int64_t* prefix,
                       const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
-                      int32_t has_mask, int64_t b, int64_t qt, int64_t kt) {
+                      int32_t has_mask, int64_t b, int64_t qt, int64_t kt) try {
   clear_error();
   if (validate_call(desc, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask) != FA_OK) return -1;
   if (b < 0 || b >= desc->B || qt < 0) {
@@ -596,20 +608,25 @@ int32_t fa_tile_class(const fa_desc_t* desc, const int64_t* prefix,
   }
   auto recs = decode_geometry(desc, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask);
   return tile_class(recs[(size_t)b], qt, kt);
+} catch (const std::exception& e) {
+  host_exception(e);
+  return -1;
 }
 
 fa_status_t fa_split_queries(const fa_desc_t* desc, const int64_t* actual_seq_qlen,
                              const int64_t* actual_seq_kvlen, int32_t n_parts,
                              const int64_t* cuts, int32_t part, fa_split_part_t* out,
-                             int64_t* out_seq_qlen, int64_t* out_seq_kvlen) {
+                             int64_t* out_seq_qlen, int64_t* out_seq_kvlen) try {
   clear_error();
   return split_queries(desc, actual_seq_qlen, actual_seq_kvlen, n_parts, cuts, part, out,
                        out_seq_qlen, out_seq_kvlen);
+} catch (const std::exception& e) {
+  return host_exception(e);
 }
 
 fa_status_t fa_plan_stats(const fa_desc_t* desc, const int64_t* prefix,
                           const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
-                          int32_t has_mask, int64_t* out) {
+                          int32_t has_mask, int64_t* out) try {
   clear_error();
   if (!out) return fail(FA_ERR_NULLPTR, "out is NULL");
   fa_status_t st = validate_call(desc, prefix, actual_seq_qlen, actual_seq_kvlen, has_mask);
@@ -634,11 +651,13 @@ fa_status_t fa_plan_stats(const fa_desc_t* desc, const int64_t* prefix,
   out[2] = counts[FA_TILE_PARTIAL];
   out[3] = counts[FA_TILE_FULL];
   return FA_OK;
+} catch (const std::exception& e) {
+  return host_exception(e);
 }
 
 fa_status_t fa_plan_items(const fa_desc_t* desc, const int64_t* prefix,
                           const int64_t* actual_seq_qlen, const int64_t* actual_seq_kvlen,
-                          int32_t num_sms, int64_t capacity, int32_t* out, int64_t* n_items) {
+                          int32_t num_sms, int64_t capacity, int32_t* out, int64_t* n_items) try {
   clear_error();
   if (!n_items) return fail(FA_ERR_NULLPTR, "n_items is NULL");
   if (capacity < 0) return fail(FA_ERR_PARAM_INVALID, "capacity %lld < 0", (long long)capacity);
@@ -661,6 +680,8 @@ fa_status_t fa_plan_items(const fa_desc_t* desc, const int64_t* prefix,
     out[4 * m + 3] = items[m].cost;
   }
   return FA_OK;
+} catch (const std::exception& e) {
+  return host_exception(e);
 }
 
 }  // extern "C"

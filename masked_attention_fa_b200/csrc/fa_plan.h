@@ -1,6 +1,7 @@
 // Host-only planning interface (validation, geometry decode, work list).
 #pragma once
 
+#include <exception>
 #include <vector>
 
 #include "../../include/fa.h"
@@ -9,6 +10,9 @@
 namespace fa {
 
 fa_status_t fail(fa_status_t st, const char* fmt, ...);
+// No C++ exception leaves a C entry point: what a failed host allocation throws
+// becomes a status there.
+fa_status_t host_exception(const std::exception& e);
 void clear_error();
 const char* last_error();
 
