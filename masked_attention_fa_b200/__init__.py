@@ -292,7 +292,11 @@ def fa_fwd_alibi(h, q, k, v, slopes, o, lse, prefix=None, actual_seq_qlen=None,
 def _relbias(table, bucket_of):
     """(fa_relbias_t, the int32 array it points into) of a table [num_buckets,
     N] and a bucket map of 2 * reach + 1 entries."""
-    m = np.ascontiguousarray(bucket_of, dtype=np.int32)
+    m = np.asarray(bucket_of)
+    if m.dtype != np.int32:  # a cast would cut fractions off and wrap large numbers
+        if m.size and not (m.min() >= 0 and m.max() < 2 ** 31 and (m == np.floor(m)).all()):
+            raise ValueError("the bucket map must hold whole numbers in [0, num_buckets)")
+    m = np.ascontiguousarray(m, dtype=np.int32)
     if m.ndim != 1 or m.size < 3 or m.size % 2 == 0:
         raise ValueError("the bucket map must have 2 * reach + 1 entries, reach >= 1")
     b = fa_relbias_t(table.data_ptr(), m.__array_interface__["data"][0], table.shape[0],
