@@ -188,6 +188,19 @@ class _Arrays:
         return self._p(self.prefix), self._p(self.cu_q), self._p(self.cu_kv)
 
 
+def _need_lengths(desc, prefix, cu_q, cu_kv):
+    """The library reads B entries of every array that the problem takes."""
+    takes = []
+    if desc.sparse_mode in (5, 6):
+        takes.append(("prefix", prefix))
+    if desc.layout == FA_TND:
+        takes += [("actual_seq_qlen", cu_q), ("actual_seq_kvlen", cu_kv)]
+    for name, a in takes:
+        n = desc.B if a is None else a.size if isinstance(a, np.ndarray) else len(a)
+        if n < desc.B:
+            raise ValueError(f"{name} has {n} entries, the problem {desc.B} batch entries")
+
+
 # ---------------------------------------------------------------- C names
 
 def fa_version() -> int:
@@ -200,12 +213,14 @@ def fa_last_error() -> str:
 
 def fa_validate(desc, prefix=None, actual_seq_qlen=None, actual_seq_kvlen=None, has_mask=False):
     """Status code of the host-side checks (0 = valid)."""
+    _need_lengths(desc, prefix, actual_seq_qlen, actual_seq_kvlen)
     a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
     return int(load_library().fa_validate(ctypes.byref(desc), *a.ptrs(), int(bool(has_mask))))
 
 
 def fa_visible_pairs(desc, prefix=None, actual_seq_qlen=None, actual_seq_kvlen=None,
                      has_mask=False) -> int:
+    _need_lengths(desc, prefix, actual_seq_qlen, actual_seq_kvlen)
     a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
     out = ctypes.c_int64(0)
     _check(load_library().fa_visible_pairs(ctypes.byref(desc), *a.ptrs(), int(bool(has_mask)),
@@ -215,6 +230,7 @@ def fa_visible_pairs(desc, prefix=None, actual_seq_qlen=None, actual_seq_kvlen=N
 
 def fa_tile_class(desc, b, qt, kt, prefix=None, actual_seq_qlen=None, actual_seq_kvlen=None,
                   has_mask=False) -> int:
+    _need_lengths(desc, prefix, actual_seq_qlen, actual_seq_kvlen)
     a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
     return int(load_library().fa_tile_class(ctypes.byref(desc), *a.ptrs(), int(bool(has_mask)),
                                              int(b), int(qt), int(kt)))
@@ -225,6 +241,7 @@ def fa_plan_items(desc, prefix=None, actual_seq_qlen=None, actual_seq_kvlen=None
     num_sms SMs: int32 array [n, 4] of (sequence, head, 256-row block, cost
     key)."""
     import numpy as np
+    _need_lengths(desc, prefix, actual_seq_qlen, actual_seq_kvlen)
     a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
     n = ctypes.c_int64(0)
     lib = load_library()
@@ -241,6 +258,7 @@ def fa_plan_items(desc, prefix=None, actual_seq_qlen=None, actual_seq_kvlen=None
 def fa_plan_stats(desc, prefix=None, actual_seq_qlen=None, actual_seq_kvlen=None,
                   has_mask=False):
     """(work items, EMPTY, PARTIAL, FULL) of the scheduler for one call."""
+    _need_lengths(desc, prefix, actual_seq_qlen, actual_seq_kvlen)
     a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
     out = (ctypes.c_int64 * 4)()
     _check(load_library().fa_plan_stats(ctypes.byref(desc), *a.ptrs(), int(bool(has_mask)), out))
@@ -440,6 +458,7 @@ def fa_fwd_noalloc(desc, q, k, v, o, lse, atten_mask=None, prefix=None, actual_s
         stream = torch.cuda.current_stream(q.device).cuda_stream
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
+    _need_lengths(desc, prefix, actual_seq_qlen, actual_seq_kvlen)
     a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
     _check(load_library().fa_fwd_noalloc(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v),
                                          _ptr(atten_mask), *a.ptrs(), _ptr(o), _ptr(lse),
@@ -469,6 +488,7 @@ def fa_split_queries(desc, actual_seq_qlen, actual_seq_kvlen, n_parts, part, cut
     [q_begin, q_end) and key range [kv_begin, kv_end) in the unsplit tensors,
     and its cumulative length arrays.
     """
+    _need_lengths(desc, None, actual_seq_qlen, actual_seq_kvlen)
     a = _Arrays(None, actual_seq_qlen, actual_seq_kvlen)
     c = None if cuts is None else np.ascontiguousarray(cuts, dtype=np.int64)
     out = fa_split_part_t()
@@ -511,6 +531,7 @@ class MaskedAttention:
                  actual_seq_kvlen=None, out=None, lse=None, stream=None, ranges=None,
                  slopes=None, rel_bias=None, rel_buckets=None):
         import torch
+        _need_lengths(self.desc, prefix, actual_seq_qlen, actual_seq_kvlen)
         if rel_bias is not None:
             return self._relbias_forward(q, k, v, rel_bias, rel_buckets, atten_mask, ranges,
                                          slopes, prefix, actual_seq_qlen, actual_seq_kvlen, out,
@@ -641,6 +662,7 @@ class MaskedAttention:
         fa_bwd in include/fa.h). d_o, d_lse: the gradients of o and lse (d_lse
         None: 0)."""
         import torch
+        _need_lengths(self.desc, prefix, actual_seq_qlen, actual_seq_kvlen)
         self._no_mask_beside(slopes, atten_mask)
         bf16, f32, dev, need = torch.bfloat16, torch.float32, q.device, self._need
         oshape, kshape, lshape = self._oshape, self._kshape, self._lshape
@@ -692,6 +714,7 @@ class MaskedAttention:
               prefix=None, out=None, lse=None, stream=None):
         """O, lse of a TND handle with K/V in paged caches (see fa_fwd_paged)."""
         import torch
+        _need_lengths(self.desc, prefix, actual_seq_qlen, actual_seq_kvlen)
         oshape, lshape = self.out_shapes()
         if out is None:
             out = torch.empty(oshape, dtype=torch.bfloat16, device=q.device)
