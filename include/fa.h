@@ -212,7 +212,10 @@ fa_status_t fa_fwd_alibi(fa_handle_t h, const void* q, const void* k, const void
  * diagonal anchored at the bottom-right corner, as in FA_ALIBI_RIGHT. The
  * pages name no such bias; the map covers one- and two-sided, linear and
  * logarithmic buckets alike.
- * table      device fp32 [num_buckets, N] (an embedding's weight), finite.
+ * table      device fp32 [num_buckets, N] (an embedding's weight), of at most 2^127
+ *            in magnitude: the scores are held in log2 units, in which larger
+ *            ones overflow. Below -2^127 (a mask of -FLT_MAX) a pair has no
+ *            weight, and a row of nothing else is a row that sees nothing.
  * bucket_of  host int32[2 * reach + 1], each in [0, num_buckets).
  * Limits: 1 <= reach <= 1024, 1 <= num_buckets <= 4096 (FA_ERR_UNSUPPORTED
  * beyond). Distances past the reach take the buckets of its two ends.
