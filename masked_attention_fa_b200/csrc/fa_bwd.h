@@ -67,7 +67,7 @@ FA_HD TileRange key_tile_rows(const SeqRec& s, int64_t c0) {
   return t;
 }
 
-// Sums of the bias's gradient by distance that a query tile writes: entry e
+// Sums of the bias's gradient by distance that a key tile writes: entry e
 // stands for the distance e - reach - kRelPad (a tile that holds a distance
 // inside (-reach, reach) reaches up to 254 past either end).
 FA_HD int32_t rel_width(int32_t reach) { return 2 * reach + 1 + 2 * kRelPad; }

@@ -84,9 +84,10 @@ constexpr int kSumRow = kCols + 32;  // bias gradient: diagonals of 32 rows x kC
 constexpr int kBwdBiasNone = 0, kBwdBiasAlibi = 1, kBwdBiasRel = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 // Of 8 pairs of columns, how many take the FMA-pipe exponential. At head dim
-// 64 the exponentials bound a step (0: 638, 2: 630, 4: 663 us on the bias
-// backward of 2 x 16 x 4096 x 64); at 128 the power cap does, and the MUFU unit
-// needs less (0: 457, 3: 463 us on a causal 2 x 16 x 4096 x 128).
+// 64 the exponentials bound a step (0: 500, 1: 484, 2: 473 us on 2 x 16 x 4096 x
+// 64 without a mask; 584, 573, 566 with the learned bias, whose 4: 30 us more); at
+// 128 the power cap does, and the MUFU unit needs less (0: 457, 3: 463 us on a
+// causal 2 x 16 x 4096 x 128).
 template <int D>
 constexpr int kPolyOf8 = D == 64 ? 2 : 0;
 template <int D>
@@ -164,7 +165,8 @@ __device__ __forceinline__ void mul_x2(float& a, float& b, float x, float y) {
 // degree kDeg for 2^f on [0, 1), p(f) = 1 + f r(f), as 2^n + (2^n f) r(f) with the
 // float 2^n whose exponent field is n + 127: exact, 0 for x < -126 (a masked
 // pair) and NaN for NaN (n added into p's exponent field instead would carry
-// NaN into a finite value). Relative error 3.0e-6 (degree 4) and 1.6e-7 (degree 5); coefficients from
+// NaN into a finite value; that was 465 us against 473 on the case at kPolyOf8).
+// Relative error 3.0e-6 (degree 4) and 1.6e-7 (degree 5); coefficients from
 // gen_exp2_poly.py.
 template <int kDeg>
 __device__ __forceinline__ void ex2_floor_x2(float& a, float& b) {
@@ -664,7 +666,7 @@ __device__ void bwd_math(const BwdParams& p, BCtl* ctl, uint32_t tmem, const uin
     for (int s = 0; s < it.hi - it.lo; ++s, ++n) {
       const int t = kKeys ? it.hi - 1 - s : it.lo + s;
       const bool partial = !(t >= it.full_lo && t < it.full_hi);
-      const int c0 = t * 128 + kCols * g;  // first column of this half
+      const int c0 = t * 128 + kCols * g;  // this group's first column
       // Distance key - diagonal of the row's column 0; it grows with the
       // column in the query walk and falls with it in the key walk.
       const int rel0 = kKeys ? at - (c0 + delta) : c0 - (at + delta);

@@ -13,7 +13,7 @@
 // depend on which one that is.
 //
 // Measured on 8 x 16 heads, one row against 8,191 keys of dimension 128 (537
-// MB, 82 us at the card's copy rate): 96 us, 5.6 TB/s, against 131 us by the
+// MB, 82 us at the card's copy rate): 96 us, 5.6 TB/s, against 120 us by the
 // tensor-core kernel. Three keys a thread group, three CTAs an SM: 2 keys 102,
 // 4 keys (two CTAs) 104 us; loads a step ahead and one softmax step for all
 // keys in flight 100 against 109; heads-first order of the grid 96 against 100.
@@ -25,7 +25,7 @@
 namespace fa {
 namespace {
 
-constexpr int kSlice = 8;      // dimensions per thread (16: 106 us against 96, see below)
+constexpr int kSlice = 8;      // dimensions per thread (16: 106 us against 96)
 constexpr int kWarps = 8;
 constexpr int kPad = 4;        // a partial row: o[D], m, l, two pad floats
 constexpr float kLn2 = 0.69314718055994530942f;

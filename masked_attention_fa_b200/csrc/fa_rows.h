@@ -14,10 +14,11 @@ namespace fa {
 constexpr int kFewRows = 4;  // query rows of a sequence it can take
 // Whether a call of `groups` = B * N pairs whose sequences have at most
 // max_rows query rows takes it. One row: always (8 x 16 heads against 8,191
-// keys of dimension 128: 96 us against 122 by the tensor-core kernel). More
-// rows: the sums over a key's threads add up (189 against 122 us), and only
-// what the split brings where the pairs leave SMs idle is worth it (2 x 8 heads,
-// 4 rows, 2,000 keys of dimension 64: 14 against 39 us). The grid, groups times
+// keys of dimension 128: 96 us against 120 by the tensor-core kernel, calls back
+// to back; 1 x 16 heads 29 against 113). More rows: the sums over a key's threads
+// add up (4 rows on the first: 190 against 120 us), and only what the split brings
+// where the pairs leave SMs idle is worth it (2 x 8 heads, 4 rows, 2,000 keys of
+// dimension 64: 20 against 40 us, caches flushed). The grid, groups times
 // at most 128 splits, stays below 2^31.
 inline bool few_rows(int32_t max_rows, int64_t groups, int num_sms) {
   return groups < (1 << 24) && (max_rows <= 1 || (max_rows <= kFewRows && 2 * groups <= num_sms));
