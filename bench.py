@@ -182,7 +182,8 @@ def kernel_label(w, dense, dev):
     sms = torch.cuda.get_device_properties(dev).multi_processor_count
     claim = (not dense) and items >= fa.CLAIM_MIN_ITEMS_PER_CTA * sms
     tf = lambda x: "true" if x else "false"
-    return (f"fa_fwd_sm100<{w.D}, true, {tf(dense)}, {tf(claim)}, {tf(w.alibi is not None)}>")
+    bias = 0 if w.alibi is None else 1  # of none, ALiBi, the learned bias
+    return f"fa_fwd_sm100<{w.D}, true, {tf(dense)}, {tf(claim)}, {bias}>"
 
 
 def visible_pairs(w, has_mask, mask_host=None):
