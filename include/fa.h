@@ -145,6 +145,11 @@ fa_status_t fa_create(const fa_desc_t* desc, fa_handle_t* out);
  *              visible key.
  * cuda_stream  a cudaStream_t (NULL = legacy default stream).
  *
+ * A NaN or infinite visible score makes its row's O and lse NaN. A hidden pair
+ * has the weight 0, whatever its score; but 0 times NaN or infinity is NaN, so V
+ * must be finite at hidden keys too where a row sees others of the same 128 keys
+ * (tokens of other packed sequences do not count).
+ *
  * Per-call constraints (sparseMode=7/8 sections): mode 7 needs, for the last
  * sequence with Sq_b > 0: pre >= Skv_b and Sq_b - Skv_b <= next <= 0, and
  * Sq_b <= Skv_b for every other sequence; mode 8 needs, for the first
@@ -264,7 +269,8 @@ fa_status_t fa_fwd_relbias(fa_handle_t h, const void* q, const void* k, const vo
  * d_lse        device fp32, shape of lse: the gradient of lse, or NULL (0).
  * dq, dk, dv   device bf16, shapes of q, k and v; every element is written.
  *              Rows that see no key get dq = 0 and add nothing to dk and dv,
- *              keys that no row sees get 0.
+ *              keys that no row sees get 0 (of finite operands: see fa_fwd; it
+ *              holds for the rows of q and d_o as for those of k and v).
  * All device operands 16-byte aligned, lse and d_lse 4-byte. The gradients may
  * overlap neither an operand nor each other (FA_ERR_PARAM_INVALID). Operands of a
  * side without tokens (Sq or Skv 0) may be NULL.
