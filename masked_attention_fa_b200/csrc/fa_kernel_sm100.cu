@@ -1220,12 +1220,13 @@ __device__ void softmax_role(const FwdParams& p, Ctl<Cfg<D>::kStages>* ctl, floa
     inv_l_sm[sub * kTileM + row] = l > 0.f ? rcp_fast(l) : 0.f;
     mbar_arrive(&ctl->epi_full[sub]);
     if (row_valid) {
-      // The sum is 0 only where no key is visible; a NaN score makes it, and lse, NaN.
-      float lse = l == 0.f ? -INFINITY : (m_used + lg2_fast(l)) * 0.69314718055994530942f;
+      // A row that sees nothing has the sum 0, whose logarithm is -inf; a NaN
+      // score makes the sum, and lse, NaN.
+      float lse = (m_used + lg2_fast(l)) * 0.69314718055994530942f;
       // Left-aligned ALiBi: the same weights, every score larger by
       // slope * (i + Skv - Sq) than the right-aligned one computed here.
       if constexpr (kAlibi)
-        if (p.alibi == 3 && l != 0.f) lse = fmaf(slope, (float)(-dbase), lse);
+        if (p.alibi == 3) lse = fmaf(slope, (float)(-dbase), lse);
       st_global_na_f32(p.lse + it.b * p.l_sb + it.h * p.l_sh + sr.q_off + i, lse);
     }
     if (stamper) FA_STAMP(sub ? 7 : 5, 7, k);
