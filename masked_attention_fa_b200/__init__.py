@@ -11,6 +11,7 @@ The C entry points keep their names (``fa_create``, ``fa_fwd``, ...). The
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -288,14 +289,9 @@ def fa_fwd(h, q, k, v, o, lse, atten_mask=None, prefix=None, actual_seq_qlen=Non
            actual_seq_kvlen=None, stream=None):
     """Enqueue one forward on `stream` (torch.cuda.Stream, raw handle int, or
     None = torch's current stream). Tensors must be CUDA tensors."""
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device).cuda_stream
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
     a = _Arrays(prefix, actual_seq_qlen, actual_seq_kvlen)
     _check(load_library().fa_fwd(h, _ptr(q), _ptr(k), _ptr(v), _ptr(atten_mask), *a.ptrs(),
-                                 _ptr(o), _ptr(lse), ctypes.c_void_p(int(stream))))
+                                 _ptr(o), _ptr(lse), _stream_int(stream, q.device)))
 
 
 def fa_fwd_alibi(h, q, k, v, slopes, o, lse, prefix=None, actual_seq_qlen=None,
@@ -397,7 +393,7 @@ def _stream_int(stream, device):
     if type(stream) is int:
         return stream
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(device.index)
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)
@@ -518,6 +514,8 @@ class MaskedAttention:
         # What the calls compare and pass, worked out once.
         self._lib = load_library()
         (self._oshape, self._lshape), self._kshape = self.out_shapes(), self.kv_shape()
+        self._takes_lengths = self.desc.sparse_mode in (5, 6) or self.desc.layout == FA_TND
+        self._room = {s: math.prod(s) for s in (self._oshape, self._lshape, self._kshape)}
 
     def out_shapes(self):
         d = self.desc
@@ -531,31 +529,38 @@ class MaskedAttention:
                  actual_seq_kvlen=None, out=None, lse=None, stream=None, ranges=None,
                  slopes=None, rel_bias=None, rel_buckets=None):
         import torch
-        _need_lengths(self.desc, prefix, actual_seq_qlen, actual_seq_kvlen)
+        if self._takes_lengths:
+            _need_lengths(self.desc, prefix, actual_seq_qlen, actual_seq_kvlen)
         if rel_bias is not None:
             return self._relbias_forward(q, k, v, rel_bias, rel_buckets, atten_mask, ranges,
                                          slopes, prefix, actual_seq_qlen, actual_seq_kvlen, out,
                                          lse, stream)
         self._no_mask_beside(slopes, atten_mask, ranges)
-        oshape, lshape = self.out_shapes()
+        oshape, lshape = self._oshape, self._lshape
         if out is None:
             out = torch.empty(oshape, dtype=torch.bfloat16, device=q.device)
         if lse is None:
             lse = torch.empty(lshape, dtype=torch.float32, device=q.device)
-        for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-            if t.dtype != torch.bfloat16 or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor")
-        if not lse.is_contiguous() or lse.dtype != torch.float32:
-            raise ValueError("lse must be a contiguous fp32 tensor")
+        dev, kshape, bf16, room = q.device, self._kshape, torch.bfloat16, self._need_room
+        if not q.is_cuda:
+            raise ValueError("q must be a contiguous bf16 CUDA tensor")
+        room("q", q, oshape, bf16, dev)
+        room("k", k, kshape, bf16, dev)
+        room("v", v, kshape, bf16, dev)
+        room("out", out, oshape, bf16, dev)
+        room("lse", lse, lshape, torch.float32, dev)
         if atten_mask is not None:
             if atten_mask.dtype not in (torch.uint8, torch.bool) or not atten_mask.is_contiguous():
                 raise ValueError("atten_mask must be a contiguous uint8/bool tensor")
+            if self._mask_shape() is not None:
+                room("atten_mask", atten_mask, self._mask_shape(), atten_mask.dtype, dev)
         if slopes is not None:
-            if slopes.dtype != torch.float32 or not slopes.is_contiguous() or not slopes.is_cuda:
-                raise ValueError("slopes must be a contiguous fp32 CUDA tensor")
+            room("slopes", slopes, (self.desc.N,), torch.float32, dev)
             fa_fwd_alibi(self.handle, q, k, v, slopes, out, lse, prefix, actual_seq_qlen,
                          actual_seq_kvlen, stream)
         elif ranges is not None:
+            if self._mask_shape() is not None:
+                room("ranges", ranges, occupancy_shapes(self.desc)[1], torch.int32, dev)
             fa_fwd_with_ranges(self.handle, q, k, v, out, lse, atten_mask, ranges, stream)
         else:
             fa_fwd(self.handle, q, k, v, out, lse, atten_mask, prefix, actual_seq_qlen,
@@ -574,6 +579,16 @@ class MaskedAttention:
         d = self.desc
         return {FA_MASK_SS: (d.Sq, d.Skv), FA_MASK_B1SS: (d.B, 1, d.Sq, d.Skv),
                 FA_MASK_BNSS: (d.B, d.N, d.Sq, d.Skv)}.get(d.mask_kind)
+
+    def _need_room(self, name, t, shape, dtype, device):
+        """t must be contiguous, of this dtype and on `device`, with the elements of
+        `shape` (or more, such as a buffer for longer calls): the library reads
+        and writes that many."""
+        if (t.dtype is dtype and t.device == device and t.is_contiguous()
+                and (t.shape == shape or t.numel() >= (self._room.get(shape) or math.prod(shape)))):
+            return
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {tuple(shape)} "
+                         f"on {device}")
 
     @staticmethod
     def _need(name, t, shape, dtype, device):
@@ -662,7 +677,8 @@ class MaskedAttention:
         fa_bwd in include/fa.h). d_o, d_lse: the gradients of o and lse (d_lse
         None: 0)."""
         import torch
-        _need_lengths(self.desc, prefix, actual_seq_qlen, actual_seq_kvlen)
+        if self._takes_lengths:
+            _need_lengths(self.desc, prefix, actual_seq_qlen, actual_seq_kvlen)
         self._no_mask_beside(slopes, atten_mask)
         bf16, f32, dev, need = torch.bfloat16, torch.float32, q.device, self._need
         oshape, kshape, lshape = self._oshape, self._kshape, self._lshape
@@ -714,17 +730,20 @@ class MaskedAttention:
               prefix=None, out=None, lse=None, stream=None):
         """O, lse of a TND handle with K/V in paged caches (see fa_fwd_paged)."""
         import torch
-        _need_lengths(self.desc, prefix, actual_seq_qlen, actual_seq_kvlen)
+        if self._takes_lengths:
+            _need_lengths(self.desc, prefix, actual_seq_qlen, actual_seq_kvlen)
         oshape, lshape = self.out_shapes()
         if out is None:
             out = torch.empty(oshape, dtype=torch.bfloat16, device=q.device)
         if lse is None:
             lse = torch.empty(lshape, dtype=torch.float32, device=q.device)
-        for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out)):
-            if t.dtype != torch.bfloat16 or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor")
-        if block_table.dtype != torch.int32 or not block_table.is_contiguous():
-            raise ValueError("block_table must be a contiguous int32 tensor")
+        if not q.is_cuda:
+            raise ValueError("q must be a contiguous bf16 CUDA tensor")
+        for name, t, shape, dtype in (
+                ("q", q, oshape, torch.bfloat16), ("k_cache", k_cache, (), torch.bfloat16),
+                ("v_cache", v_cache, (), torch.bfloat16), ("out", out, oshape, torch.bfloat16),
+                ("lse", lse, lshape, torch.float32), ("block_table", block_table, (), torch.int32)):
+            self._need_room(name, t, shape, dtype, q.device)
         d = self.desc
         if (k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape)
                 or k_cache.shape[2] != d.N or k_cache.shape[3] != d.D):
@@ -740,6 +759,11 @@ class MaskedAttention:
     def occupancy(self, atten_mask, stream=None):
         """Run the dense-mask pre-pass on its own: (tile classes, ranges);
         pass the ranges back as ``attn(..., ranges=ranges)`` to skip it."""
+        if self._mask_shape() is not None:
+            if not atten_mask.is_cuda or atten_mask.element_size() != 1:
+                raise ValueError("atten_mask must be a contiguous uint8/bool CUDA tensor")
+            self._need_room("atten_mask", atten_mask, self._mask_shape(), atten_mask.dtype,
+                            atten_mask.device)
         return fa_mask_occupancy(self.desc, atten_mask, stream=stream)
 
     def sync_status(self):
