@@ -197,7 +197,7 @@ def _need_lengths(desc, prefix, cu_q, cu_kv):
     if desc.layout == FA_TND:
         takes += [("actual_seq_qlen", cu_q), ("actual_seq_kvlen", cu_kv)]
     for name, a in takes:
-        n = desc.B if a is None else a.size if isinstance(a, np.ndarray) else len(a)
+        n = desc.B if a is None else len(a) if isinstance(a, (list, tuple)) else np.asarray(a).size
         if n < desc.B:
             raise ValueError(f"{name} has {n} entries, the problem {desc.B} batch entries")
 

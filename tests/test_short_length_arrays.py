@@ -50,3 +50,7 @@ def test_others_are_accepted():
     assert fa.fa_validate(desc, prefix=[1], **FULL) == 0
     assert fa.fa_validate(fa.make_desc(**dict(PREFIX, sparse_mode=2)), prefix=[1],
                           actual_seq_qlen=[3]) == 0
+    one = fa.make_desc(**dict(PREFIX, B=1))
+    assert fa.fa_validate(one, prefix=7) == 0  # a number stands for an array of one
+    assert fa.fa_validate(one, prefix=torch.tensor([7])) == 0
+    assert fa.fa_validate(one, prefix=np.array([[7]])) == 0
